@@ -1,5 +1,5 @@
 /*
- * moe.h - C ABI of libmoe.so, a B200 (sm_100a) MoE-layer forward pass.
+ * moe.h - C ABI of libmoe.so, a B200 (sm_100a) MoE layer: forward pass and gradients.
  *
  * The layer (shared by DiT-MoE, EC-DiT, MMOE and the DES dLLM block):
  *   router GEMM + softmax      -> affinities A in R^{T x E}
@@ -451,8 +451,201 @@ MOE_API int moe_forward_host(const moe_config *cfg, const void *x_host,
                      int32_t *dev_status, void *ws, size_t ws_bytes,
                      moe_stream_t stream);
 
+/* ------------------------------------------------------------- training
+ *
+ * Gradients of the layer's steps and the norms around a block. They follow
+ * the conventions above. Gradients shaped like activations or expert
+ * weights are in the layer dtype, rounded once from fp32; gradients of the
+ * router, of constant experts, of norm weights and of conditions are fp32.
+ * Every sum runs in a fixed order, so repeated calls give the same bits.
+ * Outputs are written, not accumulated into.
+ *
+ * A training step of the layer (each step's inputs are the forward's):
+ *   moe_combine_backward       dy -> dy_perm, dw, dconst
+ *   moe_grouped_mlp_backward   dy_perm, dy -> dx_perm, dW1, dW2, dx_shared, ...
+ *   moe_router_backward        dw -> dlogits, dz_prev, dbias, dW_r, dx_router
+ *   moe_dispatch_backward      dx_perm + dx_shared + dx_router + dy -> dx
+ */
+
+/* Workspace bytes the four backward entry points need for `cfg` (one buffer
+ * of this size serves them one after the other). */
+MOE_API int moe_backward_workspace_size(const moe_config *cfg, size_t *bytes);
+
+/*
+ * Gradient of moe_combine. With E_a(x_s) the output of assignment a's
+ * expert for its token s (the row y_perm[row_of[a]], x_s, 0, the constant
+ * vector or the mixed constant expert), y_s = sum_a w_a E_a(x_s) + ... has
+ *   dy_perm[row_of[a]] = w_a dy_s      (heavy experts)
+ *   dw[a]              = <dy_s, E_a(x_s)>
+ *   dconst             = sum_a w_a dy_s  per constant expert; with const_mix
+ *     (E = a0 x + a1 v, g = w_a dy_s): dv = sum a1 g, dWc_0 = sum q x_s,
+ *     dWc_1 = -dWc_0, q = a0 a1 (<g, x_s> - <g, v>)
+ * The residual's and the shared output's gradients are dy itself; the x_s
+ * terms of identity and mixed constant experts are in moe_dispatch_backward.
+ *   dy       [T, d] (dtype)       y_perm, x, const_vecs as in moe_combine
+ *   sel, w, row_of                as in moe_combine (expert choice: sel = tok)
+ *   dy_perm  [n_assign, d] out (dtype); rows that no assignment has are left
+ *            as they were. Must not overlap dy or y_perm.
+ *   dw       [n_assign] fp32 out; 0 for a dropped or empty assignment
+ *   dconst   [n_const, d] ([n_const, 3, d] with const_mix) fp32 out, nullable
+ * An out-of-range token id (expert choice) sets MOE_DEV_BAD_TOKEN, an
+ * out-of-range expert id other than -1 sets MOE_DEV_BAD_EXPERT; both get
+ * dw 0 and add nothing.
+ */
+MOE_API int moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm,
+                         const int32_t *sel, const float *w, const int32_t *row_of,
+                         const void *x, const void *const_vecs, void *dy_perm, float *dw,
+                         float *dconst, int32_t *dev_status, void *ws, size_t ws_bytes,
+                         moe_stream_t stream);
+
+/*
+ * Gradient of moe_dispatch's row gather, and of the x_s terms of the
+ * combine, back in token order, with up to three [T, d] gradients that
+ * reach x on other ways (the residual's, the shared expert's, the router's)
+ * added in the same pass:
+ *   dx_s = add0_s + add1_s + add2_s + sum_a { dx_perm[row_of[a]]  (heavy),
+ *          w_a dy_s (identity), a0 g + q (Wc_0 - Wc_1) (mixed constant) }
+ * summed in fp32 in that order and rounded once; g and q as above.
+ *   dx_perm  [n_assign, d] (dtype), nullable when n_heavy == 0
+ *   dy, x    [T, d]; dy is needed with identity or mixed constant experts,
+ *            x and const_vecs with mixed constant experts, else nullable
+ *   add0..2  [T, d] (dtype), nullable; dx may be the same buffer as any of
+ *            them
+ *   tok_ptr, tok_assign  expert choice: the token lists of moe_dispatch
+ */
+MOE_API int moe_dispatch_backward(const moe_config *cfg, const void *dx_perm, const void *dy,
+                          const int32_t *sel, const float *w, const int32_t *row_of,
+                          const int32_t *tok_ptr, const int32_t *tok_assign, const void *x,
+                          const void *const_vecs, const void *add0, const void *add1,
+                          const void *add2, void *dx, int32_t *dev_status,
+                          moe_stream_t stream);
+
+/*
+ * Gradient of the router and of the selected weights. The selection itself
+ * has no gradient; w_a = A[s, e] (renormalised over the token's slots with
+ * renorm under token choice, A / S with S their sum) gives
+ *   dA     = dprobs + the dw of each (s, e); renorm: (dw_a - sum_b dw_b w_b) / S
+ *   dz     = A (dA - <A, dA>)          z = x W_r^T + bias + scale z_prev
+ *   dx     = dz W_r,  dW_r = dz^T x,  dbias = sum_s dz,  dz_prev = scale dz
+ *   probs    [T, E] fp32 (A)           sel, w, tok_ptr, tok_assign: the
+ *            selection and (expert choice) its token lists
+ *   dw       [n_assign] fp32           dprobs [T, E] fp32, nullable: a
+ *            gradient that reaches A directly (a load-balance loss)
+ *   dlogits  [T, E] fp32 out (dz)      dz_prev [T, E] fp32 out, nullable
+ *   dbias    [E] fp32 out, nullable    dW_r [E, d] fp32 out, nullable
+ *   dx       [T, d] (dtype) out, nullable
+ * An empty slot (-1) adds nothing; another out-of-range expert id, or an
+ * out-of-range entry of the token lists, adds nothing and sets
+ * MOE_DEV_BAD_EXPERT. W_r is needed for dx, x for dW_r. renorm with another
+ * routing than token choice has no meaning in the layer and is ignored.
+ */
+MOE_API int moe_router_backward(const moe_config *cfg, const void *x, const void *W_r,
+                        const float *probs, const int32_t *sel, const float *w,
+                        const float *dw, const int32_t *tok_ptr, const int32_t *tok_assign,
+                        const float *dprobs, float *dlogits, float *dz_prev, float *dbias,
+                        float *dW_r, void *dx, int32_t *dev_status, void *ws,
+                        size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Gradient of moe_grouped_mlp. The hidden activations are formed again from
+ * x_perm (moe_grouped_mlp keeps none). Per expert, with X, dY its rows,
+ * U = X W1^T, H = act(U):
+ *   dH = dY W2,  dU = dH act'(U),  dX = dU W1,  dW2 = dY^T H,  dW1 = dU^T X
+ * (SwiGLU: U = [g, u], H = silu(g) u, dU = [dH u silu'(g), dH silu(g)]),
+ * and the same for the shared expert(s) over x and dy_shared. An expert
+ * without rows gets zero weight gradients. bf16 layers accumulate in fp32
+ * and keep H and dU in bf16, one rounding each; fp32 layers keep fp32.
+ *   x_perm, offsets, W1, W2, x, Ws1, Ws2   as in moe_grouped_mlp
+ *   dy_perm   [n_assign, d]         dy_shared [T, d]
+ *   dx_perm   [n_assign, d] out     rows past offsets[n_heavy] left as they were
+ *   dW1, dW2, dWs1, dWs2            shaped and typed like the weights
+ *   dx_shared [T, d] out
+ * Any output may be NULL: what only it needs is not computed. Inputs that
+ * no given output needs may be NULL too when all routed (or all shared)
+ * outputs are.
+ */
+MOE_API int moe_grouped_mlp_backward(const moe_config *cfg, const void *x_perm,
+                             const int32_t *offsets, const void *W1, const void *W2,
+                             const void *dy_perm, const void *x, const void *Ws1,
+                             const void *Ws2, const void *dy_shared, void *dx_perm,
+                             void *dW1, void *dW2, void *dx_shared, void *dWs1,
+                             void *dWs2, int32_t *dev_status, void *ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/*
+ * The norms after and before a block, fused with the block's gate and
+ * residual scale and with the next block's modulation (the adaptive norms
+ * around a diffusion transformer's layers). With h the block's output and x
+ * its residual stream, per token s and its condition row b = s / group_size:
+ *   y = res_scale x + gate_b * (N_post(h) * post_gamma)
+ *   z = (N_pre(y) * pre_gamma + pre_beta) * (1 + scale_b) + shift_b
+ * N is the identity (MOE_NORM_NONE), (v - mean) / sqrt(var + eps)
+ * (MOE_NORM_LAYER) or v / sqrt(mean v^2 + eps) (MOE_NORM_RMS). y is rounded
+ * once; z is formed from the unrounded y. A missing weight or condition
+ * (NULL) is 1 or 0.
+ *   T, d        tokens and width (d a multiple of 8, at most 8192)
+ *   group_size  tokens that share a condition row; 0: one row for all
+ *   pre_kind, post_kind, eps (> 0), res_scale
+ */
+enum moe_norm_kind { MOE_NORM_NONE = 0, MOE_NORM_LAYER = 1, MOE_NORM_RMS = 2 };
+typedef struct moe_norm_config {
+  int32_t T, d, dtype, group_size;
+  int32_t pre_kind, post_kind;
+  float eps, res_scale;
+} moe_norm_config;
+
+/*
+ *   h, x        [T, d], either nullable (no block: z = N_pre(res_scale x);
+ *               no residual: y = gate u)
+ *   post_gamma, pre_gamma, pre_beta  [d], nullable
+ *   gate, scale, shift  rows of d values, cond_stride elements apart (a
+ *               multiple of 8, at least d): chunks of one projection; nullable
+ *   y, z        [T, d] out, either nullable; z needs pre_kind. y may be the
+ *               same buffer as x or h.
+ * All in the config's dtype, 16-byte aligned.
+ */
+MOE_API int moe_block_norm(const moe_norm_config *cfg, const void *h, const void *x,
+                   const void *post_gamma, const void *gate, const void *pre_gamma,
+                   const void *pre_beta, const void *scale, const void *shift,
+                   int64_t cond_stride, void *y, void *z, moe_stream_t stream);
+
+/* Workspace bytes of moe_block_norm_backward. */
+MOE_API int moe_block_norm_workspace_size(const moe_norm_config *cfg, size_t *bytes);
+
+/*
+ * Gradient of moe_block_norm from dz and dy, the gradients of its outputs
+ * (dy: what reaches y on other ways, the next residual). The rows' means and
+ * scales are formed again from y and h.
+ *   t  = dy + dN_pre(dz (1 + scale) pre_gamma; y),   dx = res_scale t
+ *   dh = dN_post(t gate post_gamma; h)
+ *   dN(g; v) = r (g - mean(g) - n mean(g n)), n = N(v), r its scale (RMS
+ *   norms have no mean(g))
+ * and, summed over the tokens of a condition row (conditions) or all tokens
+ * (weights): dshift = dz, dscale = dz (n pre_gamma + pre_beta),
+ * dgate = t N_post(h) post_gamma, dpre_gamma = dz (1 + scale) n,
+ * dpre_beta = dz (1 + scale), dpost_gamma = t gate N_post(h).
+ *   h           nullable when dh, dgate and dpost_gamma are
+ *   y           [T, d] (the forward's y), nullable when dz is
+ *   dz, dy      [T, d], one of them nullable
+ *   dh, dx      [T, d] out, nullable; may be the same buffer as dz or dy
+ *               (not as one another)
+ *   dpost_gamma, dpre_gamma, dpre_beta  [d] fp32 out, nullable
+ *   dgate, dscale, dshift  fp32 out, rows dcond_stride floats apart (a
+ *               multiple of 4, at least d), nullable
+ * Gradients of dz's side (dscale, dshift, dpre_*) are refused without dz.
+ */
+MOE_API int moe_block_norm_backward(const moe_norm_config *cfg, const void *h, const void *y,
+                            const void *post_gamma, const void *gate, const void *pre_gamma,
+                            const void *pre_beta, const void *scale, int64_t cond_stride,
+                            const void *dz, const void *dy, void *dh, void *dx,
+                            float *dpost_gamma, float *dgate, float *dpre_gamma,
+                            float *dpre_beta, float *dscale, float *dshift,
+                            int64_t dcond_stride, void *ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
+
 
 #endif /* MOE_H_ */

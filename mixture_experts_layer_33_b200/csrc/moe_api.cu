@@ -6,6 +6,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "backward.h"
 #include "common.cuh"
 #include "internal.h"
 
@@ -17,13 +18,6 @@ int num_sms() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
   return n;
 }
-
-namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline int elem_bytes(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
 int64_t n_assign_of(const moe_config &c) {
   if (c.routing == MOE_EXPERT_CHOICE) return (int64_t)(c.T / c.group_size) * c.E * c.capacity;
@@ -88,6 +82,13 @@ int n_const_of(const moe_config &c) {
   for (int e = 0; e < c.E; ++e) n += c.expert_kind[e] == MOE_CONST;
   return n;
 }
+
+namespace {
+
+constexpr size_t kAlign = 256;
+inline size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int elem_bytes(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
 // Workspace layout shared by the entry points.
 struct Layout {

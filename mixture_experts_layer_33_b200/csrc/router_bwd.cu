@@ -1,0 +1,406 @@
+// Gradient of the router: routing weights back through the selection and the
+// softmax to the logits, the router weights, the bias and x.
+//
+// EC-DiT: Scaling Diffusion Transformers with Adaptive Expert-Choice
+// Routing, section 3: A = softmax(x W_r); a selected expert is weighted by
+// its affinity A[s, e]. MMOE, "gate-residual routing": the logits take the
+// previous layer's as a scaled term.
+//   dA = dprobs + scatter(dw),  dz = A (dA - <A, dA>)
+//   dx = dz W_r,  dW_r = dz^T x,  dbias = sum_s dz,  dz_prev = scale dz
+//
+// Two products with one narrow side (E <= 128) each: bound by reading x and
+// writing dx once, not by their FLOPs. So after a per-token kernel for dz, a
+// CTA owns 128 columns and a range of tokens: per 64-token tile it holds the
+// x and W_r columns in shared memory, forms the dx tile (K = E) and adds to
+// its dW_r block (K = 64 tokens), which stays in registers until the range
+// ends. The token ranges' blocks are summed in order by a last launch.
+// bf16 layers multiply on bf16 mma.sync (as the router's forward does: N = E
+// is far too narrow for a tcgen05 tile). dz is fp32 and enters as the sum of
+// three bf16 terms (8 mantissa bits each, 24 in all), so the products keep
+// fp32 accuracy while x and W_r are exact.
+#include "backward.h"
+#include "mma_sync.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int TT = 64;   // tokens per tile
+constexpr int TC = 128;  // columns per CTA (bf16)
+constexpr int FC = 64;   // columns per CTA (fp32)
+
+// dz of one token per warp; lane holds experts lane + 32 v.
+template <int VPL>
+__global__ void __launch_bounds__(kThreads) router_dz_kernel(RouterBwdArgs a) {
+  const int lane = threadIdx.x & 31;
+  const bool ec = a.routing == MOE_EXPERT_CHOICE;
+  const bool renorm = a.renorm && a.routing == MOE_TOKEN_TOPK;
+  for (int64_t s = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); s < a.T; s += (int64_t)gridDim.x * kWarps) {
+    float A[VPL], dA[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int e = lane + 32 * v;
+      A[v] = e < a.E ? a.probs[s * a.E + e] : 0.f;
+      dA[v] = (e < a.E && a.dprobs) ? a.dprobs[s * a.E + e] : 0.f;
+    }
+    int64_t j0, j1;
+    if (ec) {
+      j0 = a.tok_ptr[s];
+      j1 = a.tok_ptr[s + 1];
+      if (j0 < 0 || j1 < j0 || j1 > a.n_assign) {
+        if (lane == 0) set_status(a.dev_status, MOE_DEV_BAD_EXPERT);
+        j0 = j1 = 0;
+      }
+    } else {
+      j0 = s * a.k;
+      j1 = j0 + a.k;
+    }
+    // Renormalised weights w = A / S: dA = (dw - sum dw w) / S.
+    float inner = 0.f, inv = 1.f;
+    if (renorm) {
+      float S = 0.f;
+      for (int64_t j = j0 + lane; j < j1; j += 32) {
+        const int e = a.sel[j];
+        if (e >= 0 && e < a.E) {
+          S += a.probs[s * a.E + e];
+          inner = fmaf(a.dw[j], a.w[j], inner);
+        }
+      }
+      S = warp_sum(S);
+      inner = warp_sum(inner);
+      inv = 1.f / S;
+    }
+    for (int64_t b = j0; b < j1; b += 32) {
+      int e = -1;
+      float g = 0.f;
+      if (b + lane < j1) {
+        int64_t asg = b + lane;
+        if (ec) {
+          asg = a.tok_assign[asg];
+          if (asg >= 0 && asg < a.n_assign) e = (int)((asg / a.C) % a.E);
+        } else {
+          e = a.sel[asg];
+        }
+        if (e >= 0 && e < a.E) g = (a.dw[asg] - inner) * inv;
+        else if (ec || e != -1) set_status(a.dev_status, MOE_DEV_BAD_EXPERT);
+        if (e >= a.E) e = -1;
+      }
+      const int n = (int)(j1 - b < 32 ? j1 - b : 32);
+      for (int j = 0; j < n; ++j) {
+        const int ej = __shfl_sync(0xffffffffu, e, j);
+        const float gj = __shfl_sync(0xffffffffu, g, j);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+          if (ej == lane + 32 * v) dA[v] += gj;
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) dot = fmaf(A[v], dA[v], dot);
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const int e = lane + 32 * v;
+      if (e >= a.E) continue;
+      const float dz = A[v] * (dA[v] - dot);
+      a.dlogits[s * a.E + e] = dz;
+      if (a.dz_prev) a.dz_prev[s * a.E + e] = a.zscale * dz;
+    }
+  }
+}
+
+// Four 8x8 blocks, each transposed: fragments of an operand stored K first.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void *p) {
+  const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(s));
+}
+__device__ __forceinline__ void mma2(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+  mma_bf16_16816(c0, a, {b[0], b[1]});
+  mma_bf16_16816(c1, a, {b[2], b[3]});
+}
+
+// MT: E padded to 16 MT experts. Shared memory, bf16, rows padded by 8 to
+// spread ldmatrix rows over the banks: the x tile [TT][TC], the W_r columns
+// [16 MT][TC], dz as three terms [3][TT][16 MT]; the dx tile goes out
+// through the x tile's space.
+template <int MT> struct RbSmem {
+  static constexpr int EP = 16 * MT;
+  static constexpr int XP = TC + 8, ZP = EP + 8;
+  static constexpr size_t x = 0;
+  static constexpr size_t w = x + (size_t)TT * XP * 2;
+  static constexpr size_t z = w + (size_t)EP * XP * 2;
+  static constexpr size_t total = z + (size_t)3 * TT * ZP * 2;
+};
+
+template <int MT>
+__global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs a, int splits) {
+  using S = RbSmem<MT>;
+  constexpr int EP = S::EP, XP = S::XP, ZP = S::ZP;
+  extern __shared__ __align__(16) uint8_t sm[];
+  __nv_bfloat16 *sx = reinterpret_cast<__nv_bfloat16 *>(sm + S::x);
+  __nv_bfloat16 *sw = reinterpret_cast<__nv_bfloat16 *>(sm + S::w);
+  __nv_bfloat16 *sz = reinterpret_cast<__nv_bfloat16 *>(sm + S::z);
+  const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
+  const __nv_bfloat16 *wr = static_cast<const __nv_bfloat16 *>(a.W_r);
+  __nv_bfloat16 *dx = static_cast<__nv_bfloat16 *>(a.dx);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c0 = blockIdx.x * TC, split = blockIdx.y;
+  const int tiles = (a.T + TT - 1) / TT;
+  const int t_lo = (int)((int64_t)tiles * split / splits), t_hi = (int)((int64_t)tiles * (split + 1) / splits);
+  const uint4 zero4 = make_uint4(0, 0, 0, 0);
+  const bool want_w = a.dW_r != nullptr, want_x = dx != nullptr;
+
+  if (want_x)
+    for (int i = tid; i < EP * (TC / 8); i += kThreads) {
+      const int e = i / (TC / 8), c = (i % (TC / 8)) * 8;
+      *reinterpret_cast<uint4 *>(sw + e * XP + c) =
+          (e < a.E && c0 + c < a.d) ? *reinterpret_cast<const uint4 *>(wr + (size_t)e * a.d + c0 + c) : zero4;
+    }
+  float acc[MT][2][4];  // dW_r: all 16 MT experts x this warp's 16 columns
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+  float bias_sum = 0.f;  // thread e < E of column block 0
+
+  for (int t = t_lo; t < t_hi; ++t) {
+    const int s0 = t * TT;
+    __syncthreads();
+    if (want_w)
+      for (int i = tid; i < TT * (TC / 8); i += kThreads) {
+        const int r = i / (TC / 8), c = (i % (TC / 8)) * 8;
+        const bool in = s0 + r < a.T && c0 + c < a.d;
+        cp_async16(sx + r * XP + c, in ? x + (size_t)(s0 + r) * a.d + c0 + c : x, in);
+      }
+    for (int i = tid; i < TT * EP; i += kThreads) {
+      const int r = i / EP, e = i % EP;
+      const float z = (s0 + r < a.T && e < a.E) ? a.dlogits[(size_t)(s0 + r) * a.E + e] : 0.f;
+      const __nv_bfloat16 h = __float2bfloat16_rn(z);
+      const float z1 = z - __bfloat162float(h);
+      const __nv_bfloat16 m = __float2bfloat16_rn(z1);
+      sz[r * ZP + e] = h;
+      sz[(TT + r) * ZP + e] = m;
+      sz[(2 * TT + r) * ZP + e] = __float2bfloat16_rn(z1 - __bfloat162float(m));
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    if (a.dbias && blockIdx.x == 0 && tid < a.E) {
+      const int n = min(TT, a.T - s0);
+      for (int r = 0; r < n; ++r) bias_sum += a.dlogits[(size_t)(s0 + r) * a.E + tid];
+    }
+    if (want_w) {
+      // dW_r[e][c] += sum_r dz[r][e] x[r][c]: A = dz^T (ldmatrix.trans on
+      // [token][expert] rows), B = x (ldmatrix.trans on [token][column] rows).
+#pragma unroll
+      for (int k = 0; k < TT; k += 16) {
+        uint32_t b[4];  // columns 16 warp + {0..7, 8..15}, k halves
+        ldmatrix_x4_trans(b, sx + (k + (lane & 15)) * XP + warp * 16 + (lane >> 4) * 8);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint32_t f[4];
+            ldmatrix_x4_trans(f, sz + (p * TT + k + (lane & 7) + ((lane >> 4) << 3)) * ZP + m * 16 + ((lane >> 3) & 1) * 8);
+            mma2(acc[m][0], acc[m][1], f, b);
+          }
+      }
+    }
+    if (want_x) {
+      // dx[r][c] = sum_e dz[r][e] W_r[e][c]: warp (rows 16 (warp & 3), columns 64 (warp >> 2)).
+      float o[8][4];
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+      const int r0 = (warp & 3) * 16, cw = (warp >> 2) * 64;
+#pragma unroll
+      for (int k = 0; k < EP; k += 16) {
+        uint32_t f[3][4];
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          ldmatrix_x4(f[p], sz + (p * TT + r0 + (lane & 15)) * ZP + k + (lane >> 4) * 8);
+#pragma unroll
+        for (int n = 0; n < 8; n += 2) {
+          uint32_t b[4];
+          ldmatrix_x4_trans(b, sw + (k + (lane & 15)) * XP + cw + n * 8 + (lane >> 4) * 8);
+#pragma unroll
+          for (int p = 0; p < 3; ++p) mma2(o[n], o[n + 1], f[p], b);
+        }
+      }
+      __syncthreads();  // the x tile has been read by every warp
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int r = r0 + (lane >> 2), c = cw + n * 8 + (lane & 3) * 2;
+        *reinterpret_cast<__nv_bfloat162 *>(sx + r * XP + c) = __floats2bfloat162_rn(o[n][0], o[n][1]);
+        *reinterpret_cast<__nv_bfloat162 *>(sx + (r + 8) * XP + c) = __floats2bfloat162_rn(o[n][2], o[n][3]);
+      }
+      __syncthreads();
+      for (int i = tid; i < TT * (TC / 8); i += kThreads) {
+        const int r = i / (TC / 8), c = (i % (TC / 8)) * 8;
+        if (s0 + r < a.T && c0 + c < a.d)
+          *reinterpret_cast<uint4 *>(dx + (size_t)(s0 + r) * a.d + c0 + c) =
+              *reinterpret_cast<const uint4 *>(sx + r * XP + c);
+      }
+    }
+  }
+  if (want_w) {
+    float *p = a.part + (size_t)split * a.E * a.d;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int e = m * 16 + (lane >> 2), c = c0 + warp * 16 + n * 8 + (lane & 3) * 2;
+        if (c < a.d) {  // d is a multiple of 8, so c + 1 < d too
+          if (e < a.E) *reinterpret_cast<float2 *>(p + (size_t)e * a.d + c) = make_float2(acc[m][n][0], acc[m][n][1]);
+          if (e + 8 < a.E)
+            *reinterpret_cast<float2 *>(p + (size_t)(e + 8) * a.d + c) = make_float2(acc[m][n][2], acc[m][n][3]);
+        }
+      }
+  }
+  if (a.dbias && blockIdx.x == 0 && tid < a.E)
+    a.part[(size_t)(a.dW_r ? splits : 0) * a.E * a.d + (size_t)split * a.E + tid] = bias_sum;
+}
+
+// The same tiles in fp32 on CUDA cores (fp32 layers are small).
+__global__ void __launch_bounds__(kThreads) router_bwd_f32_kernel(RouterBwdArgs a, int splits) {
+  extern __shared__ __align__(16) float fm[];
+  float *sx = fm;                      // [TT][FC]
+  float *sz = sx + TT * FC;            // [TT][E]
+  float *sw = sz + TT * a.E;           // [E][FC]
+  const float *x = static_cast<const float *>(a.x);
+  const float *wr = static_cast<const float *>(a.W_r);
+  float *dx = static_cast<float *>(a.dx);
+  const int tid = threadIdx.x, c0 = blockIdx.x * FC, split = blockIdx.y;
+  const int tiles = (a.T + TT - 1) / TT;
+  const int t_lo = (int)((int64_t)tiles * split / splits), t_hi = (int)((int64_t)tiles * (split + 1) / splits);
+  const int col = tid % FC, lane4 = tid / FC;  // this thread's column, and every 4th row (expert) from lane4
+  if (dx)
+    for (int i = tid; i < a.E * FC; i += kThreads)
+      sw[i] = c0 + i % FC < a.d ? wr[(size_t)(i / FC) * a.d + c0 + i % FC] : 0.f;
+  float acc[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+  float bias_sum = 0.f;
+  for (int t = t_lo; t < t_hi; ++t) {
+    const int s0 = t * TT;
+    __syncthreads();
+    if (a.dW_r)
+      for (int i = tid; i < TT * FC; i += kThreads) {
+        const int r = s0 + i / FC, c = c0 + i % FC;
+        sx[i] = r < a.T && c < a.d ? x[(size_t)r * a.d + c] : 0.f;
+      }
+    for (int i = tid; i < TT * a.E; i += kThreads)
+      sz[i] = s0 + i / a.E < a.T ? a.dlogits[(size_t)s0 * a.E + i] : 0.f;
+    __syncthreads();
+    if (a.dbias && blockIdx.x == 0 && tid < a.E)
+      for (int r = 0; r < TT; ++r) bias_sum += sz[r * a.E + tid];
+    if (a.dW_r) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int e = lane4 + 4 * i;
+        if (e >= a.E) break;
+        float v = 0.f;  // a tile's sum on its own, then into the running one: shorter chains of rounding
+        for (int r = 0; r < TT; ++r) v = fmaf(sz[r * a.E + e], sx[r * FC + col], v);
+        acc[i] += v;
+      }
+    }
+    if (dx && c0 + col < a.d)
+      for (int r = lane4; r < TT && s0 + r < a.T; r += 4) {
+        float v = 0.f;
+        for (int e = 0; e < a.E; ++e) v = fmaf(sz[r * a.E + e], sw[e * FC + col], v);
+        dx[(size_t)(s0 + r) * a.d + c0 + col] = v;
+      }
+  }
+  if (a.dW_r && c0 + col < a.d) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int e = lane4 + 4 * i;
+      if (e >= a.E) break;
+      a.part[((size_t)split * a.E + e) * a.d + c0 + col] = acc[i];
+    }
+  }
+  if (a.dbias && blockIdx.x == 0 && tid < a.E)
+    a.part[(size_t)(a.dW_r ? splits : 0) * a.E * a.d + (size_t)split * a.E + tid] = bias_sum;
+}
+
+// Sums the token ranges in order: dW_r [E, d], then dbias [E].
+__global__ void __launch_bounds__(kThreads) router_bwd_sum_kernel(const float *part, float *dW_r, float *dbias, int E,
+                                                                  int d, int splits) {
+  const int64_t nw = dW_r ? (int64_t)E * d : 0, n = nw + (dbias ? E : 0);
+  const float *pb = part + (size_t)splits * nw;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    float v = 0.f;
+    if (i < nw) {
+#pragma unroll 8
+      for (int k = 0; k < splits; ++k) v += part[(size_t)k * nw + i];
+      dW_r[i] = v;
+    } else {
+      for (int k = 0; k < splits; ++k) v += pb[(size_t)k * E + (i - nw)];
+      dbias[i - nw] = v;
+    }
+  }
+}
+
+// Token ranges: enough CTAs (two per SM) with the columns, at least one tile
+// each, and no more partial dW_r blocks than half the bytes of x.
+int token_splits(int T, int d, int E, int dtype) {
+  const int cols = dtype == MOE_BF16 ? TC : FC, eb = dtype == MOE_BF16 ? 2 : 4;
+  const int64_t tiles = (T + TT - 1) / TT, blocks = (d + cols - 1) / cols;
+  int64_t n = (2 * 148 + blocks - 1) / blocks;
+  const int64_t cap = (int64_t)T * eb / (8 * (int64_t)E);
+  if (n > cap) n = cap;
+  if (n > tiles) n = tiles;
+  return (int)(n < 1 ? 1 : n);
+}
+
+template <int MT>
+int run_bf16(const RouterBwdArgs &a, int splits, cudaStream_t stream) {
+  const dim3 grid((a.d + TC - 1) / TC, splits);
+  MOE_CUDA_TRY(cudaFuncSetAttribute(router_bwd_bf16_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)RbSmem<MT>::total));
+  router_bwd_bf16_kernel<MT><<<grid, kThreads, RbSmem<MT>::total, stream>>>(a, splits);
+  return last_launch_status();
+}
+
+}  // namespace
+
+size_t router_bwd_workspace_bytes(int T, int d, int E, int dtype) {
+  return ((size_t)E * d + E) * 4 * token_splits(T, d, E, dtype);
+}
+
+int launch_router_bwd(const RouterBwdArgs &a, cudaStream_t stream) {
+  if (a.T > 0) {
+    int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
+    if (blocks > 8 * (int64_t)num_sms()) blocks = 8 * (int64_t)num_sms();
+    const unsigned g = (unsigned)blocks;
+    if (a.E <= 32) router_dz_kernel<1><<<g, kThreads, 0, stream>>>(a);
+    else if (a.E <= 64) router_dz_kernel<2><<<g, kThreads, 0, stream>>>(a);
+    else router_dz_kernel<4><<<g, kThreads, 0, stream>>>(a);
+  }
+  if (!a.dx && !a.dW_r && !a.dbias) return last_launch_status();
+  const int splits = token_splits(a.T, a.d, a.E, a.dtype);
+  int st = MOE_OK;
+  if (a.dtype == MOE_BF16) {
+    if (a.E <= 16) st = run_bf16<1>(a, splits, stream);
+    else if (a.E <= 32) st = run_bf16<2>(a, splits, stream);
+    else if (a.E <= 64) st = run_bf16<4>(a, splits, stream);
+    else st = run_bf16<8>(a, splits, stream);
+  } else {
+    const size_t smem = (size_t)(TT * FC + TT * a.E + a.E * FC) * 4;
+    MOE_CUDA_TRY(cudaFuncSetAttribute(router_bwd_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    router_bwd_f32_kernel<<<dim3((a.d + FC - 1) / FC, splits), kThreads, smem, stream>>>(a, splits);
+    st = last_launch_status();
+  }
+  if (st != MOE_OK || (!a.dW_r && !a.dbias)) return st;
+  int64_t blocks = ((int64_t)a.E * a.d + a.E + kThreads - 1) / kThreads;
+  if (blocks > 1184) blocks = 1184;
+  router_bwd_sum_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a.part, a.dW_r, a.dbias, a.E, a.d, splits);
+  return last_launch_status();
+}
+
+}  // namespace moe

@@ -29,6 +29,7 @@ HEAVY, IDENTITY, ZERO, CONST = 0, 1, 2, 3
 DEV_BAD_EXPERT, DEV_BAD_TOKEN, DEV_TIMEOUT, DEV_OVERFLOW, DEV_BAD_INDEX = 1, 2, 4, 8, 16
 BUILD_DEBUG = 1  # moe_build_flags() bit of the MOE_DEBUG build
 MAX_EXPERTS = 256
+NORM_NONE, NORM_LAYER, NORM_RMS = 0, 1, 2
 
 # Names of every entry point include/moe.h declares.
 ENTRY_POINTS = (
@@ -37,6 +38,9 @@ ENTRY_POINTS = (
     "moe_select_expert_choice", "moe_core_set_vote", "moe_core_set_union", "moe_dispatch",
     "moe_grouped_mlp", "moe_combine", "moe_forward", "moe_forward_host",
     "moe_dispatch_noalloc", "moe_activation", "moe_test_set_barrier_wait", "moe_build_flags",
+    "moe_backward_workspace_size", "moe_combine_backward", "moe_dispatch_backward",
+    "moe_router_backward", "moe_grouped_mlp_backward", "moe_block_norm",
+    "moe_block_norm_workspace_size", "moe_block_norm_backward",
 )
 NOALLOC_SCRATCH_BYTES = 256 * 1024  # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -54,13 +58,21 @@ class MoeConfig(ctypes.Structure):
     ]
 
 
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "d", "dtype", "group_size", "pre_kind", "post_kind")] + [
+                    ("eps", ctypes.c_float), ("res_scale", ctypes.c_float)]
+
+
 class MoeForwardAux(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("logits", "probs", "sel", "w", "votes", "core", "offsets")]
 
 
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
 _CFG = ctypes.POINTER(MoeConfig)
+_NCFG = ctypes.POINTER(MoeNormConfig)
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [_i32]),
     "moe_device_check": (_i32, [_i32]),
@@ -83,6 +95,15 @@ _SIGS = {
                            _vp]),
     "moe_forward": (_i32, [_CFG, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                            ctypes.POINTER(MoeForwardAux), _vp, _vp, _sz, _vp]),
+    "moe_backward_workspace_size": (_i32, [_CFG, ctypes.POINTER(_sz)]),
+    "moe_combine_backward": (_i32, [_CFG] + [_vp] * 11 + [_vp, _sz, _vp]),
+    "moe_dispatch_backward": (_i32, [_CFG] + [_vp] * 13 + [_vp, _vp]),
+    "moe_router_backward": (_i32, [_CFG] + [_vp] * 15 + [_vp, _sz, _vp]),
+    "moe_grouped_mlp_backward": (_i32, [_CFG] + [_vp] * 16 + [_vp, _sz, _vp]),
+    "moe_block_norm": (_i32, [_NCFG] + [_vp] * 8 + [_i64, _vp, _vp, _vp]),
+    "moe_block_norm_workspace_size": (_i32, [_NCFG, ctypes.POINTER(_sz)]),
+    "moe_block_norm_backward": (_i32, [_NCFG] + [_vp] * 7 + [_i64] + [_vp] * 10
+                                + [_i64, _vp, _sz, _vp]),
     "moe_forward_host": (_i32, [_CFG, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, _sz, _vp]),
 }
@@ -316,10 +337,202 @@ def forward_host(c: MoeConfig, x_host, W_r, W1, W2, y_host, ws, residual_host=No
                                 _dev_ptr(ws), ws.numel(), _stream(stream)), "moe_forward_host")
 
 
+# ---------------------------------------------------------------- training
+def _grad_ptr(t, what, dtype, numel):
+    """Device pointer of a tensor argument of the gradients (None stays None): dtype, size,
+    contiguity and device are checked, since a short buffer would be written past its end."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of {numel} elements, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != torch.cuda.current_device():  # -1: a host tensor
+        raise ValueError(f"{what}: expected a tensor on the current CUDA device")
+    return t.data_ptr()
+
+
+def _ws_ptr(ws):
+    return _grad_ptr(ws, "ws", torch.uint8, ws.numel())
+
+
+def _layer_dtype(c):
+    return torch.bfloat16 if c.dtype == BF16 else torch.float32
+
+
+def backward_workspace_size(c: MoeConfig) -> int:
+    n = _sz()
+    _check(LIB.moe_backward_workspace_size(ctypes.byref(c), ctypes.byref(n)),
+           "moe_backward_workspace_size")
+    return n.value
+
+
+def alloc_backward_workspace(c: MoeConfig, device="cuda"):
+    """A caller-owned workspace for the four backward entry points, which may share it as long
+    as they do not overlap on the device."""
+    return torch.empty(backward_workspace_size(c), dtype=torch.uint8, device=device)
+
+
+def _n_const(c):
+    return sum(1 for e in range(c.n_heavy, c.E) if c.expert_kind[e] == CONST)
+
+
+def combine_backward(c: MoeConfig, dy, y_perm, sel, w, row_of, tok_ptr, tok_assign, x, const_vecs,
+                     dy_perm, dw, dev_status, ws, dconst=None, stream=None):
+    """Gradient of ``combine`` (moe_combine_backward in include/moe.h). The token lists are
+    accepted for symmetry with ``combine`` and not read."""
+    n, dt, f32, i32 = num_assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    nc = _n_const(c) * (3 if c.const_mix else 1) * c.d if c.n_heavy < c.E else 0
+    _check(LIB.moe_combine_backward(
+        ctypes.byref(c), _grad_ptr(dy, "dy", dt, c.T * c.d), _grad_ptr(y_perm, "y_perm", dt, n * c.d),
+        _grad_ptr(sel, "sel", i32, n), _grad_ptr(w, "w", f32, n), _grad_ptr(row_of, "row_of", i32, n),
+        _grad_ptr(x, "x", dt, c.T * c.d), _grad_ptr(const_vecs, "const_vecs", dt, nc),
+        _grad_ptr(dy_perm, "dy_perm", dt, n * c.d), _grad_ptr(dw, "dw", f32, n),
+        _grad_ptr(dconst, "dconst", f32, nc), _grad_ptr(dev_status, "dev_status", i32, 1),
+        _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_combine_backward")
+
+
+def dispatch_backward(c: MoeConfig, dx_perm, dy, sel, w, row_of, tok_ptr, tok_assign, x, const_vecs,
+                      dx, dev_status, add=(), stream=None):
+    """Gradient of ``dispatch``'s row gather and of the combine's x terms, with up to three
+    [T, d] gradients ``add`` summed in the same pass (moe_dispatch_backward)."""
+    n, dt, f32, i32 = num_assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    nc = _n_const(c) * (3 if c.const_mix else 1) * c.d if c.n_heavy < c.E else 0
+    if len(add) > 3:
+        raise ValueError("add: at most three gradients")
+    adds = [_grad_ptr(t, "add", dt, c.T * c.d) for t in add] + [None] * (3 - len(add))
+    _check(LIB.moe_dispatch_backward(
+        ctypes.byref(c), _grad_ptr(dx_perm, "dx_perm", dt, n * c.d), _grad_ptr(dy, "dy", dt, c.T * c.d),
+        _grad_ptr(sel, "sel", i32, n), _grad_ptr(w, "w", f32, n), _grad_ptr(row_of, "row_of", i32, n),
+        _grad_ptr(tok_ptr, "tok_ptr", i32, c.T + 1), _grad_ptr(tok_assign, "tok_assign", i32, n),
+        _grad_ptr(x, "x", dt, c.T * c.d), _grad_ptr(const_vecs, "const_vecs", dt, nc), *adds,
+        _grad_ptr(dx, "dx", dt, c.T * c.d), _grad_ptr(dev_status, "dev_status", i32, 1),
+        _stream(stream)), "moe_dispatch_backward")
+
+
+def router_backward(c: MoeConfig, x, W_r, probs, sel, w, dw, tok_ptr, tok_assign, dlogits,
+                    dev_status, ws, dprobs=None, dz_prev=None, dbias=None, dW_r=None, dx=None,
+                    stream=None):
+    """Gradient of the routing weights back through selection and softmax to the logits, and
+    from there to the router's inputs (moe_router_backward)."""
+    n, dt, f32, i32 = num_assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    te = c.T * c.E
+    _check(LIB.moe_router_backward(
+        ctypes.byref(c), _grad_ptr(x, "x", dt, c.T * c.d), _grad_ptr(W_r, "W_r", dt, c.E * c.d),
+        _grad_ptr(probs, "probs", f32, te), _grad_ptr(sel, "sel", i32, n), _grad_ptr(w, "w", f32, n),
+        _grad_ptr(dw, "dw", f32, n), _grad_ptr(tok_ptr, "tok_ptr", i32, c.T + 1),
+        _grad_ptr(tok_assign, "tok_assign", i32, n), _grad_ptr(dprobs, "dprobs", f32, te),
+        _grad_ptr(dlogits, "dlogits", f32, te), _grad_ptr(dz_prev, "dz_prev", f32, te),
+        _grad_ptr(dbias, "dbias", f32, c.E), _grad_ptr(dW_r, "dW_r", f32, c.E * c.d),
+        _grad_ptr(dx, "dx", dt, c.T * c.d), _grad_ptr(dev_status, "dev_status", i32, 1),
+        _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_router_backward")
+
+
+def grouped_mlp_backward(c: MoeConfig, x_perm, offsets, W1, W2, dy_perm, x, Ws1, Ws2, dy_shared,
+                         dev_status, ws, dx_perm=None, dW1=None, dW2=None, dx_shared=None,
+                         dWs1=None, dWs2=None, stream=None):
+    """Gradient of ``grouped_mlp``; any output may be left out (moe_grouped_mlp_backward)."""
+    n, dt, i32 = num_assignments(c), _layer_dtype(c), torch.int32
+    up, hs = (2 * c.h if c.act == SWIGLU else c.h), c.n_shared * c.h_shared
+    n1, n2, ns, td = c.n_heavy * up * c.d, c.n_heavy * c.h * c.d, hs * c.d, c.T * c.d
+    _check(LIB.moe_grouped_mlp_backward(
+        ctypes.byref(c), _grad_ptr(x_perm, "x_perm", dt, n * c.d),
+        _grad_ptr(offsets, "offsets", i32, c.n_heavy + 1), _grad_ptr(W1, "W1", dt, n1),
+        _grad_ptr(W2, "W2", dt, n2), _grad_ptr(dy_perm, "dy_perm", dt, n * c.d),
+        _grad_ptr(x, "x", dt, td), _grad_ptr(Ws1, "Ws1", dt, ns), _grad_ptr(Ws2, "Ws2", dt, ns),
+        _grad_ptr(dy_shared, "dy_shared", dt, td), _grad_ptr(dx_perm, "dx_perm", dt, n * c.d),
+        _grad_ptr(dW1, "dW1", dt, n1), _grad_ptr(dW2, "dW2", dt, n2),
+        _grad_ptr(dx_shared, "dx_shared", dt, td), _grad_ptr(dWs1, "dWs1", dt, ns),
+        _grad_ptr(dWs2, "dWs2", dt, ns), _grad_ptr(dev_status, "dev_status", i32, 1),
+        _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_grouped_mlp_backward")
+
+
+# ------------------------------------------------------------- block norms
+def make_norm_config(cfg) -> MoeNormConfig:
+    """MoeNormConfig from a dict: T, d, dtype ("bf16" / "f32"), group_size (tokens per condition
+    row, 0 for one row), pre and post ("none", "layer", "rms"), eps, res_scale."""
+    kinds = {"none": NORM_NONE, "layer": NORM_LAYER, "rms": NORM_RMS}
+    return MoeNormConfig(cfg["T"], cfg["d"], BF16 if cfg["dtype"] == "bf16" else F32,
+                         cfg.get("group_size", 0), kinds[cfg.get("pre", "layer")],
+                         kinds[cfg.get("post", "none")], float(cfg.get("eps", 1e-6)),
+                         float(cfg.get("res_scale", 1.0)))
+
+
+def _cond_ptrs(n: MoeNormConfig, named, dtype):
+    """Pointers and the common row stride of condition tensors [rows, d]: chunks of one
+    projection, so rows may be further apart than d."""
+    rows = -(-n.T // n.group_size) if n.group_size else 1
+    stride, ptrs = n.d, []
+    for what, t in named:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype != dtype or tuple(t.shape) != (rows, n.d) or t.stride(1) != 1:
+            raise ValueError(f"{what}: expected {dtype} rows [{rows}, {n.d}], got {t.dtype} "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{what}: expected a tensor on the current CUDA device")
+        if rows > 1:
+            if any(p is not None for p in ptrs) and t.stride(0) != stride:
+                raise ValueError("condition tensors must have the same row stride")
+            stride = t.stride(0)
+        ptrs.append(t.data_ptr())
+    return ptrs, stride
+
+
+def block_norm(n: MoeNormConfig, h, x, y=None, z=None, post_gamma=None, gate=None, pre_gamma=None,
+               pre_beta=None, scale=None, shift=None, stream=None):
+    """y = res_scale x + gate N_post(h) post_gamma; z = (N_pre(y) pre_gamma + pre_beta)(1 + scale)
+    + shift (moe_block_norm): the end of one block and the start of the next in one pass."""
+    dt = _layer_dtype(n)
+    td = n.T * n.d
+    (gp, scp, shp), stride = _cond_ptrs(n, (("gate", gate), ("scale", scale), ("shift", shift)), dt)
+    _check(LIB.moe_block_norm(
+        ctypes.byref(n), _grad_ptr(h, "h", dt, td), _grad_ptr(x, "x", dt, td),
+        _grad_ptr(post_gamma, "post_gamma", dt, n.d), gp, _grad_ptr(pre_gamma, "pre_gamma", dt, n.d),
+        _grad_ptr(pre_beta, "pre_beta", dt, n.d), scp, shp, stride, _grad_ptr(y, "y", dt, td),
+        _grad_ptr(z, "z", dt, td), _stream(stream)), "moe_block_norm")
+
+
+def block_norm_workspace_size(n: MoeNormConfig) -> int:
+    b = _sz()
+    _check(LIB.moe_block_norm_workspace_size(ctypes.byref(n), ctypes.byref(b)),
+           "moe_block_norm_workspace_size")
+    return b.value
+
+
+def alloc_block_norm_workspace(n: MoeNormConfig, device="cuda"):
+    return torch.empty(block_norm_workspace_size(n), dtype=torch.uint8, device=device)
+
+
+def block_norm_backward(n: MoeNormConfig, h, y, dz, dy, ws, dh=None, dx=None, post_gamma=None,
+                        gate=None, pre_gamma=None, pre_beta=None, scale=None, dpost_gamma=None,
+                        dgate=None, dpre_gamma=None, dpre_beta=None, dscale=None, dshift=None,
+                        stream=None):
+    """Gradient of ``block_norm`` from dz and dy (moe_block_norm_backward)."""
+    dt, f32 = _layer_dtype(n), torch.float32
+    td = n.T * n.d
+    (gp, scp), stride = _cond_ptrs(n, (("gate", gate), ("scale", scale)), dt)
+    (dgp, dscp, dshp), dstride = _cond_ptrs(
+        n, (("dgate", dgate), ("dscale", dscale), ("dshift", dshift)), f32)
+    _check(LIB.moe_block_norm_backward(
+        ctypes.byref(n), _grad_ptr(h, "h", dt, td), _grad_ptr(y, "y", dt, td),
+        _grad_ptr(post_gamma, "post_gamma", dt, n.d), gp, _grad_ptr(pre_gamma, "pre_gamma", dt, n.d),
+        _grad_ptr(pre_beta, "pre_beta", dt, n.d), scp, stride, _grad_ptr(dz, "dz", dt, td),
+        _grad_ptr(dy, "dy", dt, td), _grad_ptr(dh, "dh", dt, td), _grad_ptr(dx, "dx", dt, td),
+        _grad_ptr(dpost_gamma, "dpost_gamma", f32, n.d), dgp,
+        _grad_ptr(dpre_gamma, "dpre_gamma", f32, n.d), _grad_ptr(dpre_beta, "dpre_beta", f32, n.d),
+        dscp, dshp, dstride, _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_block_norm_backward")
+
+
 class MoELayer:
     """A configured layer: weights and a workspace resident on one device.
 
     ``layer(x, z_prev=None)`` returns y; ``residual`` defaults to x.
+    ``layer.forward_train(x)`` runs the same layer step by step and keeps what
+    ``layer.backward`` needs to turn dy into the gradients of x, the weights
+    and the gate residual.
     """
 
     def __init__(self, cfg, weights, device="cuda"):
@@ -327,6 +540,7 @@ class MoELayer:
         self.c = make_config(cfg)
         self.w = weights
         self.ws = alloc_workspace(self.c, device)
+        self.bws = None  # the backward's workspace, made on first use
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
     def __call__(self, x, z_prev=None, residual="x", aux=None, stream=None):
@@ -337,3 +551,84 @@ class MoELayer:
                 bias=w.get("logit_bias"), Ws1=w.get("Ws1"), Ws2=w.get("Ws2"),
                 const_vecs=w.get("const_vecs"), aux=aux, dev_status=self.status, stream=stream)
         return y
+
+    def forward_train(self, x, z_prev=None, residual="x", stream=None):
+        """The layer through its stage entry points: (y, saved), ``saved`` holding the routing,
+        the dispatched rows and the expert outputs for ``backward``. ``residual`` is "x" (the
+        layer adds x), None, or another [T, d] tensor."""
+        c, w, dev, i32 = self.c, self.w, x.device, torch.int32
+        n, T, E = num_assignments(c), c.T, c.E
+        ec = c.routing == EXPERT_CHOICE
+
+        def ints(*shape):
+            return torch.empty(*shape, dtype=i32, device=dev)
+
+        s = {"x": x, "residual": residual,
+             "logits": torch.empty(T, E, device=dev), "probs": torch.empty(T, E, device=dev),
+             "sel": ints(n), "w": torch.empty(n, device=dev), "offsets": ints(c.n_heavy + 1),
+             "row_of": ints(n), "tok_ptr": ints(T + 1) if ec else None,
+             "tok_assign": ints(n) if ec else None,
+             "x_perm": torch.empty(n, c.d, dtype=x.dtype, device=dev),
+             "y_perm": torch.empty(n, c.d, dtype=x.dtype, device=dev)}
+        topk = c.routing == TOKEN_TOPK
+        router(x, w["W_r"], s["logits"], s["probs"], bias=w.get("logit_bias"), z_prev=z_prev,
+               z_prev_scale=c.gate_residual_scale, k=c.k if topk else 0, renorm=c.renorm if topk else 0,
+               idx=s["sel"] if topk else None, w=s["w"] if topk else None, stream=stream)
+        if ec:
+            select_expert_choice(s["probs"], c.group_size, c.capacity, s["sel"], s["w"], stream=stream)
+        elif c.routing == DES_VOTE:
+            votes = torch.empty(E, dtype=torch.int64, device=dev)
+            core_set_vote(s["probs"], c.k, c.M_core, votes, ints(c.M_core), s["sel"], s["w"],
+                          stream=stream)
+        elif c.routing == DES_SEQ:
+            core_set_union(s["probs"], c.k, c.k_local, ints(E), ints(1), s["sel"], s["w"], stream=stream)
+        dispatch(c, s["sel"], x, s["x_perm"], s["offsets"], ints(n), s["row_of"], s["tok_ptr"],
+                 s["tok_assign"], self.status, self.ws, stream=stream)
+        y_shared = torch.empty_like(x) if c.n_shared else None
+        grouped_mlp(c, s["x_perm"], s["offsets"], w["W1"], w["W2"], x, w.get("Ws1"), w.get("Ws2"),
+                    s["y_perm"], y_shared, self.status, self.ws, stream=stream)
+        y = torch.empty_like(x)
+        combine(c, s["y_perm"], y_shared, s["sel"], s["w"], s["row_of"], s["tok_ptr"],
+                s["tok_assign"], x, w.get("const_vecs"), x if isinstance(residual, str) else residual,
+                y, self.status, stream=stream)
+        return y, s
+
+    def backward(self, saved, dy, dprobs=None, stream=None):
+        """Gradients from dy, the gradient of ``forward_train``'s y (and ``dprobs``, a gradient
+        that reaches the affinities directly): a dict of x, W_r, logit_bias, W1, W2, Ws1, Ws2,
+        const_vecs and z_prev (those the layer has). A residual other than x has gradient dy."""
+        c, w, s, dev = self.c, self.w, saved, dy.device
+        n, x = num_assignments(c), saved["x"]
+        if self.bws is None:
+            self.bws = alloc_backward_workspace(c, dev)
+        cv = w.get("const_vecs")
+        routing = (s["sel"], s["w"], s["row_of"], s["tok_ptr"], s["tok_assign"], x, cv)
+        dy_perm, dw = torch.empty_like(s["y_perm"]), torch.empty(n, device=dev)
+        g = {"W_r": torch.empty(c.E, c.d, device=dev), "W1": torch.empty_like(w["W1"]),
+             "W2": torch.empty_like(w["W2"]), "x": torch.empty_like(x)}
+        if w.get("logit_bias") is not None:
+            g["logit_bias"] = torch.empty(c.E, device=dev)
+        if c.gate_residual_scale:
+            g["z_prev"] = torch.empty(c.T, c.E, device=dev)
+        if cv is not None:
+            g["const_vecs"] = torch.empty(cv.shape, device=dev)
+        if c.n_shared:
+            g["Ws1"], g["Ws2"] = torch.empty_like(w["Ws1"]), torch.empty_like(w["Ws2"])
+        combine_backward(c, dy, s["y_perm"], *routing, dy_perm, dw, self.status, self.bws,
+                         dconst=g.get("const_vecs"), stream=stream)
+        dx_perm = torch.empty_like(s["x_perm"])
+        dx_shared = torch.empty_like(x) if c.n_shared else None
+        grouped_mlp_backward(c, s["x_perm"], s["offsets"], w["W1"], w["W2"], dy_perm, x, w.get("Ws1"),
+                             w.get("Ws2"), dy, self.status, self.bws, dx_perm=dx_perm, dW1=g["W1"],
+                             dW2=g["W2"], dx_shared=dx_shared, dWs1=g.get("Ws1"), dWs2=g.get("Ws2"),
+                             stream=stream)
+        dx_router = torch.empty_like(x)
+        router_backward(c, x, w["W_r"], s["probs"], s["sel"], s["w"], dw, s["tok_ptr"], s["tok_assign"],
+                        torch.empty_like(s["probs"]), self.status, self.bws, dprobs=dprobs,
+                        dz_prev=g.get("z_prev"), dbias=g.get("logit_bias"), dW_r=g["W_r"], dx=dx_router,
+                        stream=stream)
+        add = [dx_router] + ([dx_shared] if c.n_shared else [])
+        if isinstance(s["residual"], str):
+            add.append(dy)
+        dispatch_backward(c, dx_perm, dy, *routing, g["x"], self.status, add=add, stream=stream)
+        return g
