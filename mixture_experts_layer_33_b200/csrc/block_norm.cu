@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(BlockNormArgs a, No
       load_or(post_gamma, c[q], col[q], 1.f, gh[q]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        gh[q][j] *= f[j];
+        gh[q][j] = col[q] ? gh[q][j] * f[j] : 0.f;  // no column past d enters the post norm's means
         S0[q][j] = S1[q][j] = P[q][j] = 0.f;
       }
     }
