@@ -74,7 +74,8 @@ struct MlpBwdProblem {
 };
 // mlp_bwd_f32.cu: fp32 layers, on CUDA cores.
 int launch_mlp_bwd_f32(const MlpBwdProblem &p, cudaStream_t stream);
-int launch_mlp_bwd_simt_bf16(const MlpBwdProblem &p, cudaStream_t stream);
+// mlp_bwd_sm100.cu: bf16 layers on tcgen05, up to two problems in each launch.
+int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStream_t stream);
 
 // block_norm.cu
 struct BlockNormArgs {

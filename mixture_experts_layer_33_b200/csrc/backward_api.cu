@@ -18,21 +18,21 @@ bool all_aligned16(P... p) {
 // One workspace for the four backward entry points, which run one after
 // another: each takes it from the start.
 struct BwdLayout {
-  size_t H, dU, U, total;  // grouped MLP; the others use it whole
+  size_t H, dU, Hs, dUs, U, total;  // grouped MLP (routed, shared); the others use it whole
 };
 BwdLayout bwd_layout(const moe_config &c) {
   BwdLayout L;
-  const size_t eb = c.dtype == MOE_BF16 ? 2 : 4;
-  const int64_t hs = (int64_t)c.n_shared * c.h_shared;
-  const size_t rr = c.n_heavy > 0 ? (size_t)n_assign_of(c) * c.h : 0, sr = (size_t)c.T * hs;
-  const size_t up = c.act == MOE_SWIGLU ? 2 : 1;
-  // Routed and shared parts run one after the other in the same buffers.
-  const size_t h = rr > sr ? rr : sr, u = up * rr > sr ? up * rr : sr;
+  const size_t eb = c.dtype == MOE_BF16 ? 2 : 4, up = c.act == MOE_SWIGLU ? 2 : 1;
+  const size_t r = c.n_heavy > 0 ? (size_t)n_assign_of(c) * c.h : 0;
+  const size_t s = (size_t)c.T * c.n_shared * c.h_shared;
   size_t o = kAlign;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes); return at; };
-  L.H = take(h * eb);
-  L.dU = take(u * eb);
-  L.U = take(u * 4);
+  L.H = take(r * eb);
+  L.dU = take(up * r * eb);
+  L.Hs = take(s * eb);
+  L.dUs = take(s * eb);
+  // The fp32 path keeps U too, of the routed and the shared part in turn.
+  L.U = take(c.dtype == MOE_F32 ? (up * r > s ? up * r : s) * 4 : 0);
   const size_t cg = const_grad_workspace_bytes(n_assign_of(c), n_const_of(c), c.d, c.const_mix);
   const size_t rt = router_bwd_workspace_bytes(c.T, c.d, c.E, c.dtype);
   if (o < kAlign + align_up(cg)) o = kAlign + align_up(cg);
@@ -194,11 +194,16 @@ int moe_grouped_mlp_backward(const moe_config *cfg, const void *x_perm, const in
     q.rows = c.T; q.n_groups = 1; q.h = (int)hs;
     q.x = x; q.dy = dy_shared; q.W1 = Ws1; q.W2 = Ws2; q.dx = dx_shared; q.dW1 = dWs1; q.dW2 = dWs2;
   }
-  for (int i = 0; i < n && st == MOE_OK; ++i) {
-    p[i].d = c.d; p[i].status = dev_status;
-    p[i].H = at<void>(ws, L.H); p[i].dU = at<void>(ws, L.dU); p[i].U = at<void>(ws, L.U);
-    st = c.dtype == MOE_F32 ? launch_mlp_bwd_f32(p[i], stream) : launch_mlp_bwd_simt_bf16(p[i], stream);
+  for (int i = 0; i < n; ++i) {
+    const bool first = i == 0 && routed;
+    p[i].d = c.d;
+    p[i].status = dev_status;
+    p[i].H = at<void>(ws, first ? L.H : L.Hs);
+    p[i].dU = at<void>(ws, first ? L.dU : L.dUs);
+    p[i].U = at<void>(ws, L.U);
   }
+  if (c.dtype == MOE_BF16) return launch_mlp_bwd_bf16(p, n, dev_status, stream);
+  for (int i = 0; i < n && st == MOE_OK; ++i) st = launch_mlp_bwd_f32(p[i], stream);
   return st;
 }
 

@@ -1,0 +1,841 @@
+// Gradient of the grouped expert MLP on Blackwell tensor cores (bf16
+// operands, fp32 accumulation in tensor memory).
+//
+// MMOE: Modernizing Diffusion Transformers with Efficient Expert Design,
+// "MoE++ expert layer": heavy experts are standard MLPs; "shared experts":
+// one dense expert is always active. With U = X W1^T, H = act(U):
+//   dH = dY W2, dU = dH act'(U), dX = dU W1, dW2 = dY^T H, dW1 = dU^T X.
+//
+// Five products of 2 rows d h FLOPs (10 and 5 with SwiGLU's 2h) in three
+// launches, each a persistent stream of 256 x 256 tiles over CTA pairs
+// (tcgen05.mma.cta_group::2, M = 256), bound by the tensor cores for large
+// groups and by the weights' bytes for small ones:
+//   act_grad   U and dH of a tile in one go. Both have K = d and the same
+//              output tile, so the tile keeps two 256-column accumulators
+//              (all 512 columns of tensor memory) and neither U nor act'(U)
+//              is written to memory or rounded: while the dH product runs,
+//              the epilogue turns U into H (stored) and act'(U), which it
+//              holds in fp32 registers; when dH is done it stores the
+//              product. The next tile's U overlaps that second half.
+//   dX         rows ragged, K = hidden width, two accumulators in turn.
+//   dW         both weight gradients (K = the group's rows) in one launch.
+//
+// Operands are stored with K contiguous (x, dy, dU as rows of the output;
+// W1 in U) or with the other dimension contiguous (W2 in dH, W1 in dX, and
+// both sides of dW); the latter are MN-major tiles of tcgen05: a TMA box is
+// 64 columns by 64 K rows, one 128-byte swizzled row per K.
+//
+// Ragged K: a group's last K block holds rows of the next group (or of
+// nothing, with any bit pattern in it), which must count as zero on both
+// sides, or a NaN there would spread. In the MN-major box a K row is one
+// 128-byte row, so the producer waits for that block's copies, clears the
+// rows past the group's end, and only then hands the block to the MMA. It is
+// the first block of a tile, so the wait overlaps the tile before.
+// Every wait is bounded: on expiry the kernel flags MOE_DEV_TIMEOUT, lets
+// its copies and MMAs in flight finish, frees tensor memory and returns.
+#include <string.h>
+
+#include <type_traits>
+
+#include "backward.h"
+#include "gemm_sched.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+constexpr int BMP = 256;                       // rows of a pair's tile
+constexpr int BN = 256;                        // columns of a tile
+constexpr int kEpiWarps = 8;                   // two per TMEM lane quadrant
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer warp, MMA warp, epilogue warps
+constexpr int STAGES = 6;
+constexpr uint32_t A_BYTES = BM * BK * 2;      // one CTA's half of A and of B
+constexpr uint32_t B_BYTES = (BN / 2) * BK * 2;
+constexpr uint32_t kStgBytes = 32 * 32 * 2;    // an epilogue warp's staging tile
+constexpr size_t kSmem = 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + kEpiWarps * kStgBytes;
+constexpr uint32_t kBox = 64 * 64 * 2;         // an MN-major box: 64 columns by 64 K rows
+
+// MN-major operand, 128-byte swizzle: 64-column blocks kBox apart (leading
+// offset), 8-row K groups 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(kBox >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+constexpr uint64_t kStepK = 2;     // descriptor units of 16 K elements, K contiguous: 32 bytes
+constexpr uint64_t kStepMn = 128;  // ... 16 K rows of 128 bytes
+constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;  // instruction descriptor: MN-major A, B
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+
+// 32 fp32 columns of this lane's row, rounded, as row `lane` of the warp's
+// 32 x 32 staging tile in the TMA 64-byte swizzle.
+__device__ __forceinline__ void stage_row(const float (&v)[32], uint32_t stg, int lane) {
+  const uint32_t row = stg + (uint32_t)lane * 64u, sw = (uint32_t)((lane >> 1) & 3);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * q + 2 * i], v[8 * q + 2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t *>(&h2);
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((uint32_t)q ^ sw) << 4)), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+  }
+}
+// The staging tile may be written: the warp's previous store has read it.
+__device__ __forceinline__ void stage_begin(int lane) {
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
+}
+// 32 columns of one row, in units of 8, those below `n` (a multiple of 8).
+__device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float (&v)[32], int n) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (8 * q < n) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = v[8 * q + i];
+      store8(o + 8 * q, f);
+    }
+}
+
+// H = GELU(u) and GELU'(u) of two values. With Q = 1 - Phi(|u|) =
+// 0.5 P(t) exp(-u^2/2) (Abramowitz & Stegun 7.1.26, as in gelu_erf_x2; the
+// error in Phi is below 1e-7) the exponential serves both:
+//   H = max(u, 0) - |u| Q,  H' = Phi(u) + u exp(-u^2/2) / sqrt(2 pi)
+__device__ __forceinline__ void gelu_and_grad_x2(float &v0, float &v1, float &g0, float &g1) {
+  const uint64_t ax = f2_pack(fabsf(v0), fabsf(v1)), v = f2_pack(v0, v1);
+  float d0, d1;
+  f2_unpack(f2_fma(ax, f2_splat(0.23164189f), f2_splat(1.0f)), d0, d1);
+  const uint64_t t = f2_pack(rcp_approx(d0), rcp_approx(d1));
+  uint64_t q = f2_fma(f2_splat(0.5307027145f), t, f2_splat(-0.7265760135f));
+  q = f2_fma(q, t, f2_splat(0.7107068705f));
+  q = f2_fma(q, t, f2_splat(-0.142248368f));
+  q = f2_fma(q, t, f2_splat(0.127414796f));
+  float s0, s1;
+  f2_unpack(f2_mul(f2_mul(v, v), f2_splat(-0.72134752044f)), s0, s1);
+  const uint64_t e = f2_pack(ex2_approx(s0), ex2_approx(s1));
+  q = f2_mul(f2_mul(q, t), e);  // 1 - Phi(|u|)
+  float q0, q1;
+  f2_unpack(q, q0, q1);
+  const uint64_t phi = f2_pack(v0 < 0.f ? q0 : 1.0f - q0, v1 < 0.f ? q1 : 1.0f - q1);
+  f2_unpack(f2_fma(f2_mul(v, f2_splat(0.3989422804f)), e, phi), g0, g1);
+  const float m0 = fmaxf(v0, 0.f), m1 = fmaxf(v1, 0.f);
+  f2_unpack(f2_fma(f2_mul(ax, f2_splat(-1.0f)), q, f2_pack(m0, m1)), v0, v1);
+}
+
+// ---------------------------------------------------------------- act_grad
+struct ActGradProb {
+  const int32_t *offsets;
+  int n_groups, h, h1;  // h1: rows of W1 per group (2h when gated)
+  int64_t rows;
+  __nv_bfloat16 *H, *dU;
+  int tma_out;
+};
+struct ActGradParams {
+  int n_probs, d;
+  ActGradProb pr[2];
+  int32_t *status;
+};
+struct ActGradMaps {
+  CUtensorMap x[2], dy[2], w1[2], w2[2], H[2], dU[2];
+};
+
+template <bool GATED>
+__global__ void __launch_bounds__(kThreads, 1)
+act_grad_kernel(const __grid_constant__ ActGradMaps tm, const __grid_constant__ ActGradParams p) {
+  constexpr int HC = GATED ? BN / 2 : BN;            // hidden columns per tile
+  constexpr uint32_t B2_BYTES = (HC / 2) * BK * 2;   // one CTA's half of W2's columns
+  constexpr uint32_t IDESC_U = idesc_bf16_f32(BMP, BN), IDESC_D = idesc_bf16_f32(BMP, HC) | kMajorB;
+  constexpr int NC = HC / 64;                        // 32-column chunks per epilogue warp
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * STAGES + 5];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ Sched sched;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = (int)cluster_id_x(), npairs = (int)nclusters_x();
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sA = smem_u32(base), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * B_BYTES;
+  const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
+  const uint32_t tfull0 = smem_u32(&bars[2 * STAGES]), tempty0 = smem_u32(&bars[2 * STAGES + 2]);
+  const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]);
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {  // accumulator 0: U, 1: dH
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (warp == 2) {
+    int run = 0, ne = 0;
+    for (int pi = 0; pi < p.n_probs; ++pi)
+      sched_add(sched, pi, p.pr[pi].offsets, p.pr[pi].n_groups, p.pr[pi].rows, BMP, (p.pr[pi].h + HC - 1) / HC,
+                p.status, run, ne);
+    sched_close(sched, p.n_probs, run, ne);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers exist before any cross-CTA arrival
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  const int nkb = (p.d + BK - 1) / BK;
+  TileSeq seq;
+  seq.init(sched, nkb, nkb, p.n_probs, pair, npairs);
+  const uint32_t leader_full0 = mapa_shared(full0, 0), leader_tempty0 = mapa_shared(tempty0, 0);
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer (both CTAs): U's K blocks, then dH's
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int t = seq.next(); ok && t >= 0; t = seq.next()) {
+      const int e = find_entry(sched, t), pi = sched.prob[e], g = sched.group[e];
+      const ActGradProb &pr = p.pr[pi];
+      const int ntn = (pr.h + HC - 1) / HC, local = t - sched.tile_start[e];
+      const int mt = local / ntn, n0 = (local - mt * ntn) * HC;
+      const int a_row = sched.row0[e] + mt * BMP + (int)rank * BM;
+      // Rank r's half of U's columns: 128 more hidden columns, or (gated) the up rows of the same ones.
+      const int w1_row = g * pr.h1 + n0 + (int)rank * (GATED ? pr.h : BN / 2);
+      const int w2_col = n0 + (int)rank * (HC / 2);
+      for (int kb = 0; ok && kb < 2 * nkb; ++kb) {
+        const bool second = kb >= nkb;
+        const int k0 = (second ? kb - nkb : kb) * BK;
+        if (!mbar_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &abort_flag, p.status)) { ok = false; break; }
+        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * (A_BYTES + (second ? B2_BYTES : B_BYTES)));
+        const uint32_t fb = leader_full0 + 8 * stage, dA = sA + stage * A_BYTES, dB = sB + stage * B_BYTES;
+        if (!second) {
+          tma_load_2d_pair(dA, &tm.x[pi], k0, a_row, fb);
+          tma_load_2d_pair(dB, &tm.w1[pi], k0, w1_row, fb);
+        } else {
+          tma_load_2d_pair(dA, &tm.dy[pi], k0, a_row, fb);
+#pragma unroll
+          for (int b = 0; b < HC / 128; ++b)
+            tma_load_3d_pair(dB + b * kBox, &tm.w2[pi], w2_col + 64 * b, k0, g, fb);
+        }
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (leader)  // the leader's full barriers count both CTAs' copies
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s))
+          mbar_wait_cluster(full0 + 8 * s, (armed_parity >> s) & 1u, &abort_flag, p.status, false);
+  } else if (warp == 1 && lane == 0) {
+    if (leader) {
+      // ---------------- MMA issuer (leader only)
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = seq.next(); ok && t >= 0; t = seq.next()) {
+        for (int a = 0; ok && a < 2; ++a) {
+          if (!mbar_wait_cluster(tempty0 + 8 * a, acc_phase ^ 1u, &abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!mbar_wait_cluster(full0 + 8 * stage, phase, &abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t adesc = smem_desc_sw128(sA + stage * A_BYTES);
+            if (a == 0) {
+              const uint64_t bdesc = smem_desc_sw128(sB + stage * B_BYTES);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                tc_mma_pair(tmem_base, adesc + kStepK * kk, bdesc + kStepK * kk, IDESC_U, (kb | kk) != 0 ? 1u : 0u);
+            } else {
+              const uint64_t bdesc = smem_desc_mn(sB + stage * B_BYTES);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)
+                tc_mma_pair(tmem_base + BN, adesc + kStepK * kk, bdesc + kStepMn * kk, IDESC_D,
+                            (kb | kk) != 0 ? 1u : 0u);
+            }
+            tc_commit_pair(empty0 + 8 * stage, 0x3);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
+          if (ok) tc_commit_pair(tfull0 + 8 * a, 0x3);
+        }
+        acc_phase ^= 1u;
+      }
+      tc_commit_pair(drain, 0x3);
+    }
+    // Every MMA that reads this CTA's shared memory or writes its TMEM has
+    // completed once the leader's last commit lands here.
+    mbar_wait_cluster(drain, 0, &abort_flag, p.status, false);
+  } else if (warp >= 2) {
+    // ---------------- epilogue (both CTAs, own TMEM rows)
+    const int quad = warp & 3, c_lo = ((warp - 2) / 4) * (HC / 2);
+    const uint32_t stg = sO + (uint32_t)(warp - 2) * kStgBytes;
+    uint32_t acc_phase = 0;
+    for (int t = seq.next(); t >= 0; t = seq.next()) {
+      const int e = find_entry(sched, t), pi = sched.prob[e];
+      const ActGradProb &pr = p.pr[pi];
+      const int ntn = (pr.h + HC - 1) / HC, local = t - sched.tile_start[e];
+      const int mt = local / ntn, n0 = (local - mt * ntn) * HC;
+      const int wrow0 = sched.row0[e] + mt * BMP + (int)rank * BM + quad * 32, row = wrow0 + lane;
+      const bool valid = row < sched.row_end[e];
+      const bool rows_tma = pr.tma_out && wrow0 + 32 <= sched.row_end[e];
+      const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16);
+      bool ready = mbar_wait_cluster(tfull0, acc_phase, &abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+      float g1[NC][32], g2[GATED ? NC : 1][32];  // act'(U) of this lane's row; gated: the factors of dg and du
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        const int c = c_lo + 32 * q, n = pr.h - (n0 + c);  // columns left of the hidden width
+        float v[32];
+        tmem_ld32(taddr + c, v);
+        if (GATED) {
+          float u[32];
+          tmem_ld32(taddr + BN / 2 + c, u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = v[i], sg = rcp_approx(1.0f + ex2_approx(-1.4426950409f * a)), s = a * sg;
+            g1[q][i] = u[i] * fmaf(sg, 1.0f - s, s);  // u silu'(a), silu' = sg + s (1 - sg) = sg (1 - s) + s
+            g2[q][i] = s;
+            v[i] = s * u[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) gelu_and_grad_x2(v[i], v[i + 1], g1[q][i], g1[q][i + 1]);
+        }
+        if (rows_tma && n >= 32) {
+          stage_begin(lane);
+          stage_row(v, stg, lane);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm.H[pi], n0 + c, wrow0, stg);
+            bulk_commit();
+          }
+        } else if (valid) {
+          store_row(pr.H + (size_t)row * pr.h + n0 + c, v, n);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_tempty0);
+      ready = mbar_wait_cluster(tfull0 + 8, acc_phase, &abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        const int c = c_lo + 32 * q, n = pr.h - (n0 + c);
+        float v[32];
+        tmem_ld32(taddr + BN + c, v);
+#pragma unroll
+        for (int part = 0; part < (GATED ? 2 : 1); ++part) {
+          float o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = v[i] * (part ? g2[GATED ? q : 0][i] : g1[q][i]);
+          const int oc = part * pr.h + n0 + c;
+          if (rows_tma && n >= 32) {
+            stage_begin(lane);
+            stage_row(o, stg, lane);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tm.dU[pi], oc, wrow0, stg);
+              bulk_commit();
+            }
+          } else if (valid) {
+            store_row(pr.dU + (size_t)row * pr.h1 + oc, o, n);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8);
+      acc_phase ^= 1u;
+    }
+    if (lane == 0) bulk_wait_all();  // every tile store has landed before the CTA exits
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+  }
+}
+
+// ------------------------------------------------------------- dX and dW
+// One product per problem, D = A . B with 256 x 256 tiles (the last columns
+// of a problem as a 256 x 128 tile when 128 are enough):
+//   RAGGED_K false (dX): D[rows, N] = A[rows, K] B_g[K, N], A K-major
+//   RAGGED_K true  (dW): D_g[M, N] = sum over the group's rows A[r, M] B[r, N],
+//                        A MN-major; an empty group's tiles are zero
+// B is MN-major in both.
+struct GemmProb {
+  const int32_t *offsets;
+  int n_groups;
+  int64_t rows;
+  int M, N, K;   // M: dW; K: dX
+  __nv_bfloat16 *out;
+  int tma_out;
+  int tile_end;  // dW: tiles of the problems up to this one
+};
+constexpr int kMaxProbs = 4;
+struct GemmParams {
+  int n_probs;
+  GemmProb pr[kMaxProbs];
+  int32_t *status;
+};
+struct GemmMaps {
+  CUtensorMap a[kMaxProbs], b[kMaxProbs], o[kMaxProbs];
+};
+
+struct Tile {
+  int pi, g, m0, n0, nw;  // m0: dX's first row, dW's first output row; nw: columns of the MMA
+  int lo, hi;             // the group's rows (dX: row_end in hi)
+  int nkb;
+};
+
+// The order of a pair's tiles: dX from the table of row tiles, dW counted
+// off problem by problem, group by group, columns fastest.
+template <bool RAGGED_K> struct Tiles;
+template <> struct Tiles<false> {
+  TileSeq seq;
+  const Sched *s;
+  __device__ void init(const Sched *sched, const GemmParams &p, int id, int n) {
+    s = sched;
+    seq.init(*s, (p.pr[0].K + BK - 1) / BK, (p.pr[1].K + BK - 1) / BK, p.n_probs, id, n);
+  }
+  __device__ bool next(const GemmParams &p, Tile &o) {
+    const int t = seq.next();
+    if (t < 0) return false;
+    const int e = find_entry(*s, t);
+    o.pi = s->prob[e];
+    o.g = s->group[e];
+    const GemmProb &pr = p.pr[o.pi];
+    const int ntn = (pr.N + BN - 1) / BN, local = t - s->tile_start[e], mt = local / ntn;
+    o.m0 = s->row0[e] + mt * BMP;
+    o.hi = s->row_end[e];
+    o.n0 = (local - mt * ntn) * BN;
+    o.nw = pr.N - o.n0 <= BN / 2 ? BN / 2 : BN;
+    o.nkb = (pr.K + BK - 1) / BK;
+    return true;
+  }
+};
+template <> struct Tiles<true> {
+  int t, step;
+  __device__ void init(const Sched *, const GemmParams &, int id, int n) { t = id; step = n; }
+  __device__ bool next(const GemmParams &p, Tile &o) {
+    int pi = 0, first = 0;
+    while (pi < p.n_probs && t >= p.pr[pi].tile_end) first = p.pr[pi++].tile_end;
+    if (pi == p.n_probs) return false;
+    const GemmProb &pr = p.pr[pi];
+    const int ntn = (pr.N + BN - 1) / BN, per = ntn * ((pr.M + BMP - 1) / BMP), local = t - first;
+    o.pi = pi;
+    o.g = local / per;
+    const int r = local - o.g * per;
+    o.m0 = (r / ntn) * BMP;
+    o.n0 = (r % ntn) * BN;
+    o.nw = pr.N - o.n0 <= BN / 2 ? BN / 2 : BN;
+    o.lo = pr.offsets ? pr.offsets[o.g] : 0;
+    o.hi = pr.offsets ? pr.offsets[o.g + 1] : (int)pr.rows;
+    check_group_rows(o.lo, o.hi, pr.rows, p.status);
+    o.nkb = (o.hi - o.lo + BK - 1) / BK;
+    t += step;
+    return true;
+  }
+};
+
+template <bool RAGGED_K>
+__global__ void __launch_bounds__(kThreads, 1)
+mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__ GemmParams p) {
+  constexpr uint32_t IDESC0 = kMajorB | (RAGGED_K ? kMajorA : 0u);
+  constexpr uint32_t IDESC_W = idesc_bf16_f32(BMP, BN) | IDESC0, IDESC_N = idesc_bf16_f32(BMP, BN / 2) | IDESC0;
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * STAGES + 6];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ typename std::conditional<RAGGED_K, char, Sched>::type sched_mem;
+  Sched *sched = reinterpret_cast<Sched *>(&sched_mem);  // dX only
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sA = smem_u32(base), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * B_BYTES;
+  const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
+  const uint32_t tfull0 = smem_u32(&bars[2 * STAGES]), tempty0 = smem_u32(&bars[2 * STAGES + 2]);
+  const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]), tail = smem_u32(&bars[2 * STAGES + 5]);
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 2);  // one arrival from each CTA's producer
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    mbar_init(tail, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (!RAGGED_K && warp == 2) {
+    int run = 0, ne = 0;
+    for (int pi = 0; pi < p.n_probs; ++pi)
+      sched_add(*sched, pi, p.pr[pi].offsets, p.pr[pi].n_groups, p.pr[pi].rows, BMP, (p.pr[pi].N + BN - 1) / BN,
+                p.status, run, ne);
+    sched_close(*sched, p.n_probs, run, ne);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers exist before any cross-CTA arrival
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  Tiles<RAGGED_K> tiles;  // the same in both CTAs of the pair
+  tiles.init(sched, p, (int)cluster_id_x(), (int)nclusters_x());
+  const uint32_t leader_full0 = mapa_shared(full0, 0), leader_tempty0 = mapa_shared(tempty0, 0);
+  Tile t;
+
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs): lane 0 issues, the warp clears a tail block
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0, tail_phase = 0;
+    bool ok = true;
+    while (ok && tiles.next(p, t)) {
+      const CUtensorMap *mA = &tm.a[t.pi], *mB = &tm.b[t.pi];
+      const int bx = t.n0 + (int)rank * (t.nw / 2), nb = t.nw / 128;  // this CTA's columns of B, in boxes
+      const int am = t.m0 + (int)rank * BM;
+      const uint32_t mine = A_BYTES + (uint32_t)nb * kBox;
+      for (int i = 0; i < t.nkb; ++i) {
+        const int kb = RAGGED_K ? t.nkb - 1 - i : i;  // a tail block first
+        const int valid = RAGGED_K ? t.hi - t.lo - kb * BK : BK;
+        int go = 1;
+        if (lane == 0) go = mbar_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &abort_flag, p.status);
+        go = __shfl_sync(0xffffffffu, go, 0);
+        if (!go) { ok = false; break; }
+        const uint32_t dA = sA + stage * A_BYTES, dB = sB + stage * B_BYTES;
+        if (valid >= BK) {
+          if (lane == 0) {
+            const uint32_t fb = leader_full0 + 8 * stage;
+            if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * mine);
+            else mbar_arrive_cluster(fb);
+            if (RAGGED_K) {
+              tma_load_2d_pair(dA, mA, am, t.lo + kb * BK, fb);
+              tma_load_2d_pair(dA + kBox, mA, am + 64, t.lo + kb * BK, fb);
+              for (int b = 0; b < nb; ++b) tma_load_2d_pair(dB + b * kBox, mB, bx + 64 * b, t.lo + kb * BK, fb);
+            } else {
+              tma_load_2d_pair(dA, mA, kb * BK, am, fb);
+              for (int b = 0; b < nb; ++b) tma_load_3d_pair(dB + b * kBox, mB, bx + 64 * b, kb * BK, t.g, fb);
+            }
+          }
+        } else {
+          // The group's last rows: into this CTA first, the rest cleared, then handed over.
+          if (lane == 0) {
+            mbar_arrive_expect_tx(tail, mine);
+            tma_load_2d(dA, mA, am, t.lo + kb * BK, tail);
+            tma_load_2d(dA + kBox, mA, am + 64, t.lo + kb * BK, tail);
+            for (int b = 0; b < nb; ++b) tma_load_2d(dB + b * kBox, mB, bx + 64 * b, t.lo + kb * BK, tail);
+          }
+          __syncwarp();
+          mbar_wait(tail, tail_phase, &abort_flag, p.status, false);
+          tail_phase ^= 1u;
+          for (int b = 0; b < 2 + nb; ++b) {
+            const uint32_t box = b < 2 ? dA + b * kBox : dB + (b - 2) * kBox;
+            for (uint32_t o = (uint32_t)valid * 128u + lane * 16u; o < kBox; o += 512u)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + o), "r"(0) : "memory");
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader_full0 + 8 * stage);
+        }
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (leader && lane == 0)  // the leader's full barriers count both CTAs' copies
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s))
+          mbar_wait_cluster(full0 + 8 * s, (armed_parity >> s) & 1u, &abort_flag, p.status, false);
+    __syncwarp();
+  } else if (warp == 1 && lane == 0) {
+    if (leader) {
+      // ---------------- MMA issuer (leader only)
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      while (ok && tiles.next(p, t)) {
+        if (t.nkb == 0) continue;  // an empty group: the epilogue stores zeros
+        if (!mbar_wait_cluster(tempty0 + 8 * acc, acc_phase ^ 1u, &abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+        const uint32_t idesc = t.nw == BN ? IDESC_W : IDESC_N;
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          if (!mbar_wait_cluster(full0 + 8 * stage, phase, &abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t adesc = RAGGED_K ? smem_desc_mn(sA + stage * A_BYTES) : smem_desc_sw128(sA + stage * A_BYTES);
+          const uint64_t bdesc = smem_desc_mn(sB + stage * B_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            tc_mma_pair(d_tmem, adesc + (RAGGED_K ? kStepMn : kStepK) * kk, bdesc + kStepMn * kk, idesc,
+                        (kb | kk) != 0 ? 1u : 0u);
+          tc_commit_pair(empty0 + 8 * stage, 0x3);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair(tfull0 + 8 * acc, 0x3);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+      tc_commit_pair(drain, 0x3);
+    }
+    mbar_wait_cluster(drain, 0, &abort_flag, p.status, false);
+  } else if (warp >= 2) {
+    // ---------------- epilogue (both CTAs, own TMEM rows)
+    const int quad = warp & 3;
+    const uint32_t stg = sO + (uint32_t)(warp - 2) * kStgBytes;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    while (tiles.next(p, t)) {
+      const GemmProb &pr = p.pr[t.pi];
+      const int wrow0 = t.m0 + (int)rank * BM + quad * 32, row = wrow0 + lane;
+      const int row_end = RAGGED_K ? pr.M : t.hi;
+      // dW's rows end with its tensor, where the TMA store clips them; dX's
+      // end inside it, so a block reaching past them is stored lane by lane.
+      const bool tma = RAGGED_K ? wrow0 < row_end : pr.tma_out && wrow0 + 32 <= row_end;
+      const int half = t.nw / 2, c_lo = ((warp - 2) / 4) * half;
+      if (t.nkb > 0) {
+        const bool ready = mbar_wait_cluster(tfull0 + 8 * acc, acc_phase, &abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, ready)) break;
+        tc_fence_after();
+      }
+      const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * BN);
+#pragma unroll 1
+      for (int c = c_lo; c < c_lo + half; c += 32) {
+        float v[32];
+        if (t.nkb > 0) {
+          tmem_ld32(taddr + c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        const int col = t.n0 + c;
+        if (col >= pr.N) continue;
+        if (tma) {
+          stage_begin(lane);
+          stage_row(v, stg, lane);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (RAGGED_K) tma_store_3d(&tm.o[t.pi], col, wrow0, t.g, stg);
+            else tma_store_2d(&tm.o[t.pi], col, wrow0, stg);
+            bulk_commit();
+          }
+        } else if (row < row_end) {
+          store_row(pr.out + (size_t)row * pr.N + col, v, pr.N - col);
+        }
+      }
+      if (t.nkb > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8 * acc);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // every tile store has landed before the CTA exits
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+  }
+}
+
+// ------------------------------------------------------------ host side
+// bf16 tensor [z, rows, cols] (z = 1: 2-D), box {bx, by}; `swizzle` 128 for
+// operands (64 columns), 64 for stored tiles (32 columns).
+bool make_map(CUtensorMap *m, const void *ptr, int64_t cols, int64_t rows, int64_t z, int bx, int by, bool store) {
+  const auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const int rank = z > 0 ? 3 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)(rows > 0 ? rows : 1), (cuuint64_t)z};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * (cuuint64_t)rows};
+  cuuint32_t box[3] = {(cuuint32_t)bx, (cuuint32_t)by, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            store ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool operand_k(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols) {  // K contiguous, 128 rows a box
+  return make_map(m, ptr, cols, rows, 0, BK, BM, false);
+}
+bool operand_mn(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t z) {
+  return make_map(m, ptr, cols, rows, z, 64, 64, false);
+}
+bool stored(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t z) {
+  return make_map(m, ptr, cols, rows, z, 32, 32, true);
+}
+
+template <auto kern, typename Maps, typename Params>
+int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cudaStream_t stream) {
+  if (max_tiles == 0) return MOE_OK;
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(2 * (unsigned)(num_sms() / 2));
+  // Co-resident CTA pairs, asked once per kernel (a function-local static is
+  // initialised once, safely under concurrent first calls).
+  static const int max_clusters = [&] {
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+    return n;
+  }();
+  int clusters = max_clusters;
+  if (clusters < 1) return MOE_ERR_UNSUPPORTED;
+  if (max_tiles < clusters) clusters = (int)max_tiles;
+  cfg.gridDim = dim3(2 * (unsigned)clusters);
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, maps, params));
+  return last_launch_status();
+}
+
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t row_tiles(const MlpBwdProblem &q) { return div_up(q.rows, BMP) + (q.offsets ? q.n_groups : 0); }
+constexpr int64_t kMaxTiles = 0x7fffffff;
+
+// Problems i of `q` with rows, in one launch (all gated or none).
+int run_act_grad(const MlpBwdProblem *q, int n, bool gated, int32_t *status, cudaStream_t stream) {
+  ActGradMaps maps;
+  ActGradParams pd;
+  memset(&maps, 0, sizeof(maps));
+  memset(&pd, 0, sizeof(pd));
+  pd.status = status;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    const MlpBwdProblem &s = q[i];
+    if (s.rows == 0 || (s.gated != 0) != gated) continue;
+    const int k = pd.n_probs++, h1 = gated ? 2 * s.h : s.h;
+    pd.d = s.d;
+    ActGradProb &o = pd.pr[k];
+    o.offsets = s.offsets; o.n_groups = s.n_groups; o.h = s.h; o.h1 = h1; o.rows = s.rows;
+    o.H = static_cast<__nv_bfloat16 *>(s.H); o.dU = static_cast<__nv_bfloat16 *>(s.dU);
+    if (!operand_k(&maps.x[k], s.x, s.rows, s.d) || !operand_k(&maps.dy[k], s.dy, s.rows, s.d) ||
+        !operand_k(&maps.w1[k], s.W1, (int64_t)s.n_groups * h1, s.d) ||
+        !operand_mn(&maps.w2[k], s.W2, s.d, s.h, s.n_groups))
+      return MOE_ERR_CUDA;
+    o.tma_out = stored(&maps.H[k], s.H, s.rows, s.h, 0) && stored(&maps.dU[k], s.dU, s.rows, h1, 0);
+    tiles += row_tiles(s) * div_up(s.h, gated ? BN / 2 : BN);
+  }
+  if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
+  return gated ? launch_pairs<act_grad_kernel<true>>(maps, pd, tiles, stream)
+               : launch_pairs<act_grad_kernel<false>>(maps, pd, tiles, stream);
+}
+
+}  // namespace
+
+int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStream_t stream) {
+  int st = run_act_grad(q, n, false, status, stream);
+  if (st == MOE_OK) st = run_act_grad(q, n, true, status, stream);
+  if (st != MOE_OK) return st;
+  GemmMaps maps;
+  GemmParams pd;
+  memset(&maps, 0, sizeof(maps));
+  memset(&pd, 0, sizeof(pd));
+  pd.status = status;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {  // dX = dU W1
+    const MlpBwdProblem &s = q[i];
+    if (!s.dx || s.rows == 0) continue;
+    const int k = pd.n_probs++, h1 = s.gated ? 2 * s.h : s.h;
+    GemmProb &o = pd.pr[k];
+    o.offsets = s.offsets; o.n_groups = s.n_groups; o.rows = s.rows; o.N = s.d; o.K = h1;
+    o.out = static_cast<__nv_bfloat16 *>(s.dx);
+    if (!operand_k(&maps.a[k], s.dU, s.rows, h1) || !operand_mn(&maps.b[k], s.W1, h1, s.d, s.n_groups))
+      return MOE_ERR_CUDA;
+    o.tma_out = stored(&maps.o[k], s.dx, s.rows, s.d, 0);
+    tiles += row_tiles(s) * div_up(s.d, BN);
+  }
+  if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
+  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>>(maps, pd, tiles, stream)) != MOE_OK) return st;
+  memset(&maps, 0, sizeof(maps));
+  memset(&pd, 0, sizeof(pd));
+  pd.status = status;
+  tiles = 0;
+  for (int i = n - 1; i >= 0; --i)   // the shared expert's long K first
+    for (int which = 0; which < 2; ++which) {
+      const MlpBwdProblem &s = q[i];
+      void *out = which ? s.dW1 : s.dW2;
+      if (!out) continue;
+      const int k = pd.n_probs++, h1 = s.gated ? 2 * s.h : s.h;
+      GemmProb &o = pd.pr[k];
+      o.offsets = s.offsets; o.n_groups = s.n_groups; o.rows = s.rows;
+      o.M = which ? h1 : s.d;  // dW1 = dU^T X, dW2 = dY^T H
+      o.N = which ? s.d : s.h;
+      o.out = static_cast<__nv_bfloat16 *>(out);
+      const void *A = which ? s.dU : s.dy, *B = which ? s.x : s.H;
+      if (s.rows > 0 && (!operand_mn(&maps.a[k], A, s.rows, o.M, 0) || !operand_mn(&maps.b[k], B, s.rows, o.N, 0)))
+        return MOE_ERR_CUDA;
+      if (!stored(&maps.o[k], out, o.M, o.N, s.n_groups)) return MOE_ERR_CUDA;
+      tiles += s.n_groups * div_up(o.M, BMP) * div_up(o.N, BN);
+      if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
+      o.tile_end = (int)tiles;
+    }
+  return launch_pairs<mlp_bwd_pair_kernel<true>>(maps, pd, tiles, stream);
+}
+
+}  // namespace moe
