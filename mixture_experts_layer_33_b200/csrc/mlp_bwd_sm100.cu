@@ -489,7 +489,7 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   constexpr uint32_t IDESC_W = idesc_bf16_f32(BMP, BN) | IDESC0, IDESC_N = idesc_bf16_f32(BMP, BN / 2) | IDESC0;
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * STAGES + 7];
+  __shared__ __align__(8) uint64_t bars[3 * STAGES + 6];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ typename std::conditional<RAGGED_K, char, Sched>::type sched_mem;
@@ -503,13 +503,16 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
   const uint32_t tfull0 = smem_u32(&bars[2 * STAGES]), tempty0 = smem_u32(&bars[2 * STAGES + 2]);
   const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]), tail = smem_u32(&bars[2 * STAGES + 5]);
-  const uint32_t peer_tail = smem_u32(&bars[2 * STAGES + 6]), leader_peer_tail = mapa_shared(peer_tail, 0);
+  // The peer's word that its part of a stage's tail block is ready, one per
+  // stage: the peer may be a ring ahead of the leader, never more.
+  const uint32_t peer_tail0 = smem_u32(&bars[2 * STAGES + 6]), leader_peer_tail0 = mapa_shared(peer_tail0, 0);
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
+      mbar_init(peer_tail0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
@@ -517,7 +520,6 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
     }
     mbar_init(drain, 1);
     mbar_init(tail, 1);
-    mbar_init(peer_tail, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -547,7 +549,7 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   if (warp == 0) {
     // ---------------- TMA producer (both CTAs): lane 0 issues, the warp clears a tail block
     int stage = 0;
-    uint32_t phase = 0, armed = 0, armed_parity = 0, tail_phase = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0, tail_phase = 0, peer_phase = 0;  // peer_phase: a bit per stage
     bool ok = true;
     auto advance = [&] {
       armed |= 1u << stage;
@@ -585,12 +587,13 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
         __syncwarp();
         if (lane == 0) {
           if (leader) {
-            ok = mbar_wait_cluster(peer_tail, tail_phase, &abort_flag, p.status);
+            ok = mbar_wait_cluster(peer_tail0 + 8 * stage, (peer_phase >> stage) & 1u, &abort_flag, p.status);
             mbar_arrive_cluster(leader_full0 + 8 * stage);
           } else {
-            mbar_arrive_cluster(leader_peer_tail);
+            mbar_arrive_cluster(leader_peer_tail0 + 8 * stage);
           }
         }
+        peer_phase ^= 1u << stage;
         tail_phase ^= 1u;
         advance();
       }

@@ -32,6 +32,10 @@ CASES = {
     "one_row": dict(d=512, h=256, act="swiglu", dtype="bf16", counts=[0, 0, 1, 0]),
     "no_rows": dict(d=64, h=72, act="gelu", dtype="bf16", counts=[0, 0, 0]),
     "many_experts": dict(d=72, h=96, act="gelu", dtype="bf16", counts=[(7 * e) % 11 for e in range(100)]),
+    # Many tiles per CTA pair, nearly all of them one tail block: the two CTAs
+    # of a pair drift apart by as much as the ring allows.
+    "many_tails": dict(d=520, h=776, act="swiglu", dtype="bf16", counts=[1 + e % 9 for e in range(128)]),
+    "tails_and_blocks": dict(d=776, h=520, act="gelu", dtype="bf16", counts=[(e * 37) % 150 for e in range(60)]),
     "f32_gelu": dict(d=72, h=136, act="gelu", dtype="f32", counts=[5, 0, 70, 1], hs=40),
     "f32_swiglu": dict(d=40, h=72, act="swiglu", dtype="f32", counts=[17, 64, 0]),
 }
