@@ -28,12 +28,12 @@
 // Ragged K: a group's last K block holds rows of the next group (or of
 // nothing, with any bit pattern in it), which must count as zero on both
 // sides, or a NaN there would spread. In the MN-major box a K row is one
-// 128-byte row, so the producer waits for that block's copies, clears the
-// rows past the group's end, and only then hands the block to the MMA. It is
-// the first block of a tile, so the wait overlaps the tile before. Only
-// these blocks need a signal from the peer CTA (a release arrival on every
-// block's barrier held both launches to half their rate: dX 587 us against
-// 251, dW 1208 against 565 on DiT-MoE-XL's experts).
+// 128-byte row, so a warp of its own waits for that block's copies, clears
+// the rows past the group's end up to the MMA's next 16, and only then hands
+// the block over. It is the first block of a tile, so the wait overlaps the
+// tile before. Only these blocks need a signal from the peer CTA (a release
+// arrival on every block's barrier held both launches to half their rate: dX
+// 587 us against 251, dW 1208 against 565 on DiT-MoE-XL's experts).
 // Every wait is bounded: on expiry the kernel flags MOE_DEV_TIMEOUT, lets
 // its copies and MMAs in flight finish, frees tensor memory and returns.
 #include <string.h>
@@ -53,11 +53,15 @@ constexpr int BMP = 256;                       // rows of a pair's tile
 constexpr int BN = 256;                        // columns of a tile
 constexpr int kEpiWarps = 8;                   // two per TMEM lane quadrant
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer warp, MMA warp, epilogue warps
+constexpr int kTailWarp = 2 + kEpiWarps;       // dW: clears the K blocks that end a group
 constexpr int STAGES = 6;
 constexpr uint32_t A_BYTES = BM * BK * 2;      // one CTA's half of A and of B
 constexpr uint32_t B_BYTES = (BN / 2) * BK * 2;
 constexpr uint32_t kStgBytes = 32 * 32 * 2;    // an epilogue warp's staging tile
-constexpr size_t kSmem = 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + kEpiWarps * kStgBytes;
+// `ns` staging tiles per epilogue warp.
+constexpr size_t smem_bytes(int ns) {
+  return 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + (size_t)ns * kEpiWarps * kStgBytes;
+}
 constexpr uint32_t kBox = 64 * 64 * 2;         // an MN-major box: 64 columns by 64 K rows
 
 // MN-major operand, 128-byte swizzle: 64-column blocks kBox apart (leading
@@ -107,9 +111,10 @@ __device__ __forceinline__ void stage_row(const float (&v)[32], uint32_t stg, in
                  : "memory");
   }
 }
-// The staging tile may be written: the warp's previous store has read it.
+// A staging tile may be written: the warp's last store but NS - 1 has read it.
+template <int NS>
 __device__ __forceinline__ void stage_begin(int lane) {
-  if (lane == 0) bulk_wait_read_all();
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(NS - 1) : "memory");
   __syncwarp();
 }
 // 32 columns of one row, in units of 8, those below `n` (a multiple of 8).
@@ -340,7 +345,7 @@ act_grad_kernel(const __grid_constant__ ActGradMaps tm, const __grid_constant__ 
           for (int i = 0; i < 32; i += 2) gelu_and_grad_x2(v[i], v[i + 1], g1[q][i], g1[q][i + 1]);
         }
         if (rows_tma && n >= 32) {
-          stage_begin(lane);
+          stage_begin<1>(lane);
           stage_row(v, stg, lane);
           fence_async_smem();
           __syncwarp();
@@ -370,7 +375,7 @@ act_grad_kernel(const __grid_constant__ ActGradMaps tm, const __grid_constant__ 
           for (int i = 0; i < 32; ++i) o[i] = v[i] * (part ? g2[GATED ? q : 0][i] : g1[q][i]);
           const int oc = part * pr.h + n0 + c;
           if (rows_tma && n >= 32) {
-            stage_begin(lane);
+            stage_begin<1>(lane);
             stage_row(o, stg, lane);
             fence_async_smem();
             __syncwarp();
@@ -482,14 +487,20 @@ template <> struct Tiles<true> {
   }
 };
 
+// dW's tiles of small groups are little more than their stores, so its
+// epilogue warps stage the next 32 columns while the last ones are read;
+// dX's tile table takes that space.
+constexpr int staging_tiles(bool ragged_k) { return ragged_k ? 2 : 1; }
+
 template <bool RAGGED_K>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads + (RAGGED_K ? 32 : 0), 1)
 mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__ GemmParams p) {
+  constexpr int NS = staging_tiles(RAGGED_K);
   constexpr uint32_t IDESC0 = kMajorB | (RAGGED_K ? kMajorA : 0u);
   constexpr uint32_t IDESC_W = idesc_bf16_f32(BMP, BN) | IDESC0, IDESC_N = idesc_bf16_f32(BMP, BN / 2) | IDESC0;
 
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[3 * STAGES + 6];
+  __shared__ __align__(8) uint64_t bars[4 * STAGES + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ typename std::conditional<RAGGED_K, char, Sched>::type sched_mem;
@@ -502,16 +513,17 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   const uint32_t sA = smem_u32(base), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * B_BYTES;
   const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
   const uint32_t tfull0 = smem_u32(&bars[2 * STAGES]), tempty0 = smem_u32(&bars[2 * STAGES + 2]);
-  const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]), tail = smem_u32(&bars[2 * STAGES + 5]);
+  const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]), tail0 = smem_u32(&bars[2 * STAGES + 5]);
   // The peer's word that its part of a stage's tail block is ready, one per
   // stage: the peer may be a ring ahead of the leader, never more.
-  const uint32_t peer_tail0 = smem_u32(&bars[2 * STAGES + 6]), leader_peer_tail0 = mapa_shared(peer_tail0, 0);
+  const uint32_t peer_tail0 = smem_u32(&bars[3 * STAGES + 5]), leader_peer_tail0 = mapa_shared(peer_tail0, 0);
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
+      mbar_init(tail0 + 8 * s, 1);
       mbar_init(peer_tail0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -519,7 +531,6 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
       mbar_init(tempty0 + 8 * a, 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
-    mbar_init(tail, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -546,62 +557,32 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   const uint32_t leader_full0 = mapa_shared(full0, 0), leader_tempty0 = mapa_shared(tempty0, 0);
   Tile t;
 
-  if (warp == 0) {
-    // ---------------- TMA producer (both CTAs): lane 0 issues, the warp clears a tail block
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer (both CTAs). A tail block goes to the
+    // CTA's own barrier of its stage; the tail warp clears it and hands it over.
     int stage = 0;
-    uint32_t phase = 0, armed = 0, armed_parity = 0, tail_phase = 0, peer_phase = 0;  // peer_phase: a bit per stage
+    uint32_t phase = 0, armed = 0, armed_parity = 0, tail_phase = 0, tail_armed = 0;
     bool ok = true;
-    auto advance = [&] {
-      armed |= 1u << stage;
-      armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-    };
     while (ok && tiles.next(p, t)) {
       const CUtensorMap *mA = &tm.a[t.pi], *mB = &tm.b[t.pi];
       const int bx = t.n0 + (int)rank * (t.nw / 2), nb = t.nw / 128;  // this CTA's columns of B, in boxes
       const int am = t.m0 + (int)rank * BM;
       const uint32_t mine = A_BYTES + (uint32_t)nb * kBox;
-      const int tail_rows = RAGGED_K ? (t.hi - t.lo) % BK : 0, full_kb = t.nkb - (tail_rows != 0);
-      if (RAGGED_K && tail_rows) {
-        // The group's last rows first: into this CTA, the rest of the block
-        // cleared; the leader hands the stage over once both have done so.
-        if (lane == 0) ok = mbar_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &abort_flag, p.status);
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        if (!ok) break;
-        const uint32_t dA = sA + stage * A_BYTES, dB = sB + stage * B_BYTES;
-        const int row = t.lo + full_kb * BK;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(tail, mine);
-          tma_load_2d(dA, mA, am, row, tail);
-          tma_load_2d(dA + kBox, mA, am + 64, row, tail);
-          for (int b = 0; b < nb; ++b) tma_load_2d(dB + b * kBox, mB, bx + 64 * b, row, tail);
-        }
-        __syncwarp();
-        mbar_wait(tail, tail_phase, &abort_flag, p.status, false);
-        for (int b = 0; b < 2 + nb; ++b) {
-          const uint32_t box = b < 2 ? dA + b * kBox : dB + (b - 2) * kBox;
-          for (uint32_t o = (uint32_t)tail_rows * 128u + lane * 16u; o < kBox; o += 512u)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + o), "r"(0) : "memory");
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader) {
-            ok = mbar_wait_cluster(peer_tail0 + 8 * stage, (peer_phase >> stage) & 1u, &abort_flag, p.status);
-            mbar_arrive_cluster(leader_full0 + 8 * stage);
-          } else {
-            mbar_arrive_cluster(leader_peer_tail0 + 8 * stage);
-          }
-        }
-        peer_phase ^= 1u << stage;
-        tail_phase ^= 1u;
-        advance();
-      }
-      if (lane == 0) {
-        for (int kb = 0; kb < full_kb; ++kb) {
-          if (!mbar_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &abort_flag, p.status)) { ok = false; break; }
+      for (int i = 0; i < t.nkb; ++i) {
+        const int kb = RAGGED_K ? t.nkb - 1 - i : i;  // a tail block first
+        if (!mbar_wait_cluster(empty0 + 8 * stage, phase ^ 1u, &abort_flag, p.status)) { ok = false; break; }
+        const uint32_t dA = sA + stage * A_BYTES, dB = sB + stage * B_BYTES, fb = leader_full0 + 8 * stage;
+        if (RAGGED_K && t.lo + kb * BK + BK > t.hi) {
+          const int row = t.lo + kb * BK;
+          const uint32_t tb = tail0 + 8 * stage;
+          mbar_arrive_expect_tx(tb, mine);
+          tma_load_2d(dA, mA, am, row, tb);
+          tma_load_2d(dA + kBox, mA, am + 64, row, tb);
+          for (int b = 0; b < nb; ++b) tma_load_2d(dB + b * kBox, mB, bx + 64 * b, row, tb);
+          tail_armed |= 1u << stage;  // the parity of this use
+          tail_phase ^= 1u << stage;
+        } else {
           if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * mine);
-          const uint32_t fb = leader_full0 + 8 * stage, dA = sA + stage * A_BYTES, dB = sB + stage * B_BYTES;
           if (RAGGED_K) {
             const int row = t.lo + kb * BK;
             tma_load_2d_pair(dA, mA, am, row, fb);
@@ -611,19 +592,52 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
             tma_load_2d_pair(dA, mA, kb * BK, am, fb);
             for (int b = 0; b < nb; ++b) tma_load_3d_pair(dB + b * kBox, mB, bx + 64 * b, kb * BK, t.g, fb);
           }
-          advance();
         }
+        // The stage's last use, of either kind: its full barrier goes no further.
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      // The other lanes follow lane 0's place in the ring.
-      stage = __shfl_sync(0xffffffffu, stage, 0);
-      phase = __shfl_sync(0xffffffffu, phase, 0);
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
-    if (leader && lane == 0)  // the leader's full barriers count both CTAs' copies
-      for (int s = 0; s < STAGES; ++s)
-        if (armed & (1u << s))
-          mbar_wait_cluster(full0 + 8 * s, (armed_parity >> s) & 1u, &abort_flag, p.status, false);
-    __syncwarp();
+    // Let every copy land before the CTA can exit: the leader's full barriers
+    // count both CTAs' copies, a tail's barrier its own CTA's.
+    for (int s = 0; s < STAGES; ++s) {
+      if (leader && (armed & (1u << s)))
+        mbar_wait_cluster(full0 + 8 * s, (armed_parity >> s) & 1u, &abort_flag, p.status, false);
+      if (tail_armed & (1u << s)) mbar_wait(tail0 + 8 * s, ((tail_phase >> s) & 1u) ^ 1u, &abort_flag, p.status, false);
+    }
+  } else if (RAGGED_K && warp == kTailWarp) {
+    // ---------------- tail warp (both CTAs): the ring stages of tail blocks, in order
+    int stage = 0;
+    uint32_t tail_phase = 0;  // a bit per stage
+    bool ok = true;
+    while (ok && tiles.next(p, t)) {
+      const int rows = (t.hi - t.lo) % BK;
+      if (rows) {
+        ok = __all_sync(0xffffffffu, mbar_wait(tail0 + 8 * stage, (tail_phase >> stage) & 1u, &abort_flag, p.status));
+        if (!ok) break;
+        // The MMA takes the block's rows in steps of 16: clear up to the next one.
+        const uint32_t lo = (uint32_t)rows * 128u, hi = (uint32_t)((rows + 15) & ~15) * 128u;
+        for (int b = 0; b < 2 + t.nw / 128; ++b) {
+          const uint32_t box = b < 2 ? sA + stage * A_BYTES + b * kBox : sB + stage * B_BYTES + (b - 2) * kBox;
+          for (uint32_t o = lo + lane * 16u; o < hi; o += 512u)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + o), "r"(0) : "memory");
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (!leader) {
+            mbar_arrive_cluster(leader_peer_tail0 + 8 * stage);
+          } else {
+            ok = mbar_wait_cluster(peer_tail0 + 8 * stage, (tail_phase >> stage) & 1u, &abort_flag, p.status);
+            mbar_arrive_cluster(leader_full0 + 8 * stage);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        tail_phase ^= 1u << stage;
+      }
+      stage = (stage + t.nkb) % STAGES;
+    }
   } else if (warp == 1 && lane == 0) {
     if (leader) {
       // ---------------- MMA issuer (leader only)
@@ -641,10 +655,14 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
           tc_fence_after();
           const uint64_t adesc = RAGGED_K ? smem_desc_mn(sA + stage * A_BYTES) : smem_desc_sw128(sA + stage * A_BYTES);
           const uint64_t bdesc = smem_desc_mn(sB + stage * B_BYTES);
+          // A tail block (the tile's first) ends at the last 16 rows that hold any of the group's.
+          const int tail_rows = RAGGED_K && kb == 0 ? (t.hi - t.lo) % BK : 0;
+          const int steps = tail_rows ? (tail_rows + 15) / 16 : BK / 16;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_pair(d_tmem, adesc + (RAGGED_K ? kStepMn : kStepK) * kk, bdesc + kStepMn * kk, idesc,
-                        (kb | kk) != 0 ? 1u : 0u);
+            if (kk < steps)
+              tc_mma_pair(d_tmem, adesc + (RAGGED_K ? kStepMn : kStepK) * kk, bdesc + kStepMn * kk, idesc,
+                          (kb | kk) != 0 ? 1u : 0u);
           tc_commit_pair(empty0 + 8 * stage, 0x3);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -655,10 +673,11 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
       tc_commit_pair(drain, 0x3);
     }
     mbar_wait_cluster(drain, 0, &abort_flag, p.status, false);
-  } else if (warp >= 2) {
+  } else if (warp >= 2 && warp < kTailWarp) {
     // ---------------- epilogue (both CTAs, own TMEM rows)
     const int quad = warp & 3;
-    const uint32_t stg = sO + (uint32_t)(warp - 2) * kStgBytes;
+    const uint32_t stg0 = sO + (uint32_t)(warp - 2) * NS * kStgBytes;
+    uint32_t stg = stg0;
     int acc = 0;
     uint32_t acc_phase = 0;
     while (tiles.next(p, t)) {
@@ -687,7 +706,7 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
         const int col = t.n0 + c;
         if (col >= pr.N) continue;
         if (tma) {
-          stage_begin(lane);
+          stage_begin<NS>(lane);
           stage_row(v, stg, lane);
           fence_async_smem();
           __syncwarp();
@@ -696,6 +715,7 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
             else tma_store_2d(&tm.o[t.pi], col, wrow0, stg);
             bulk_commit();
           }
+          if (NS > 1) stg = stg == stg0 ? stg0 + kStgBytes : stg0;
         } else if (row < row_end) {
           store_row(pr.out + (size_t)row * pr.N + col, v, pr.N - col);
         }
@@ -745,10 +765,10 @@ bool stored(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t
   return make_map(m, ptr, cols, rows, z, 32, 32, true);
 }
 
-template <auto kern, typename Maps, typename Params>
+template <auto kern, int threads, int ns, typename Maps, typename Params>
 int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cudaStream_t stream) {
   if (max_tiles == 0) return MOE_OK;
-  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(ns)));
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[1];
@@ -758,8 +778,8 @@ int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cuda
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem_bytes(ns);
   cfg.stream = stream;
   cfg.gridDim = dim3(2 * (unsigned)(num_sms() / 2));
   // Co-resident CTA pairs, asked once per kernel (a function-local static is
@@ -805,8 +825,8 @@ int run_act_grad(const MlpBwdProblem *q, int n, bool gated, int32_t *status, cud
     tiles += row_tiles(s) * div_up(s.h, gated ? BN / 2 : BN);
   }
   if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
-  return gated ? launch_pairs<act_grad_kernel<true>>(maps, pd, tiles, stream)
-               : launch_pairs<act_grad_kernel<false>>(maps, pd, tiles, stream);
+  return gated ? launch_pairs<act_grad_kernel<true>, kThreads, 1>(maps, pd, tiles, stream)
+               : launch_pairs<act_grad_kernel<false>, kThreads, 1>(maps, pd, tiles, stream);
 }
 
 }  // namespace
@@ -834,7 +854,7 @@ int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStre
     tiles += row_tiles(s) * div_up(s.d, BN);
   }
   if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
-  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>>(maps, pd, tiles, stream)) != MOE_OK) return st;
+  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>, kThreads, 1>(maps, pd, tiles, stream)) != MOE_OK) return st;
   memset(&maps, 0, sizeof(maps));
   memset(&pd, 0, sizeof(pd));
   pd.status = status;
@@ -858,7 +878,7 @@ int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStre
       if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
       o.tile_end = (int)tiles;
     }
-  return launch_pairs<mlp_bwd_pair_kernel<true>>(maps, pd, tiles, stream);
+  return launch_pairs<mlp_bwd_pair_kernel<true>, kThreads + 32, staging_tiles(true)>(maps, pd, tiles, stream);
 }
 
 }  // namespace moe
