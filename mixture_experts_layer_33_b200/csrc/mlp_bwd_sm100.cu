@@ -57,10 +57,9 @@ constexpr int kTailWarp = 2 + kEpiWarps;       // dW: clears the K blocks that e
 constexpr int STAGES = 6;
 constexpr uint32_t A_BYTES = BM * BK * 2;      // one CTA's half of A and of B
 constexpr uint32_t B_BYTES = (BN / 2) * BK * 2;
-constexpr uint32_t kStgBytes = 32 * 32 * 2;    // an epilogue warp's staging tile
-// `ns` staging tiles per epilogue warp.
-constexpr size_t smem_bytes(int ns) {
-  return 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + (size_t)ns * kEpiWarps * kStgBytes;
+constexpr uint32_t kStgBytes = 32 * 32 * 2;    // an epilogue warp's staging tile of 32 columns
+constexpr size_t smem_bytes(uint32_t staging) {
+  return 1024 + (size_t)STAGES * (A_BYTES + B_BYTES) + (size_t)kEpiWarps * staging;
 }
 constexpr uint32_t kBox = 64 * 64 * 2;         // an MN-major box: 64 columns by 64 K rows
 
@@ -111,10 +110,25 @@ __device__ __forceinline__ void stage_row(const float (&v)[32], uint32_t stg, in
                  : "memory");
   }
 }
-// A staging tile may be written: the warp's last store but NS - 1 has read it.
-template <int NS>
+// 64 columns, as row `lane` of a 32 x 64 tile in the TMA 128-byte swizzle.
+__device__ __forceinline__ void stage_row(const float (&v)[2][32], uint32_t stg, int lane) {
+  const uint32_t row = stg + (uint32_t)lane * 128u, sw = (uint32_t)(lane & 7);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h2 = __floats2bfloat162_rn(v[q >> 2][8 * (q & 3) + 2 * i], v[q >> 2][8 * (q & 3) + 2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t *>(&h2);
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((uint32_t)q ^ sw) << 4)), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+  }
+}
+// The staging tile may be written: the warp's last store has read it.
 __device__ __forceinline__ void stage_begin(int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(NS - 1) : "memory");
+  if (lane == 0) bulk_wait_read_all();
   __syncwarp();
 }
 // 32 columns of one row, in units of 8, those below `n` (a multiple of 8).
@@ -345,7 +359,7 @@ act_grad_kernel(const __grid_constant__ ActGradMaps tm, const __grid_constant__ 
           for (int i = 0; i < 32; i += 2) gelu_and_grad_x2(v[i], v[i + 1], g1[q][i], g1[q][i + 1]);
         }
         if (rows_tma && n >= 32) {
-          stage_begin<1>(lane);
+          stage_begin(lane);
           stage_row(v, stg, lane);
           fence_async_smem();
           __syncwarp();
@@ -375,7 +389,7 @@ act_grad_kernel(const __grid_constant__ ActGradMaps tm, const __grid_constant__ 
           for (int i = 0; i < 32; ++i) o[i] = v[i] * (part ? g2[GATED ? q : 0][i] : g1[q][i]);
           const int oc = part * pr.h + n0 + c;
           if (rows_tma && n >= 32) {
-            stage_begin<1>(lane);
+            stage_begin(lane);
             stage_row(o, stg, lane);
             fence_async_smem();
             __syncwarp();
@@ -487,15 +501,14 @@ template <> struct Tiles<true> {
   }
 };
 
-// dW's tiles of small groups are little more than their stores, so its
-// epilogue warps stage the next 32 columns while the last ones are read;
+// An epilogue warp's staging tile. dW's tiles of small groups are little
+// more than their stores, which go out as whole 128-byte lines (64 columns);
 // dX's tile table takes that space.
-constexpr int staging_tiles(bool ragged_k) { return ragged_k ? 2 : 1; }
+constexpr uint32_t staging_bytes(bool ragged_k) { return ragged_k ? 2 * kStgBytes : kStgBytes; }
 
 template <bool RAGGED_K>
 __global__ void __launch_bounds__(kThreads + (RAGGED_K ? 32 : 0), 1)
 mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__ GemmParams p) {
-  constexpr int NS = staging_tiles(RAGGED_K);
   constexpr uint32_t IDESC0 = kMajorB | (RAGGED_K ? kMajorA : 0u);
   constexpr uint32_t IDESC_W = idesc_bf16_f32(BMP, BN) | IDESC0, IDESC_N = idesc_bf16_f32(BMP, BN / 2) | IDESC0;
 
@@ -676,17 +689,12 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   } else if (warp >= 2 && warp < kTailWarp) {
     // ---------------- epilogue (both CTAs, own TMEM rows)
     const int quad = warp & 3;
-    const uint32_t stg0 = sO + (uint32_t)(warp - 2) * NS * kStgBytes;
-    uint32_t stg = stg0;
+    const uint32_t stg = sO + (uint32_t)(warp - 2) * staging_bytes(RAGGED_K);
     int acc = 0;
     uint32_t acc_phase = 0;
     while (tiles.next(p, t)) {
       const GemmProb &pr = p.pr[t.pi];
       const int wrow0 = t.m0 + (int)rank * BM + quad * 32, row = wrow0 + lane;
-      const int row_end = RAGGED_K ? pr.M : t.hi;
-      // dW's rows end with its tensor, where the TMA store clips them; dX's
-      // end inside it, so a block reaching past them is stored lane by lane.
-      const bool tma = RAGGED_K ? wrow0 < row_end : pr.tma_out && wrow0 + 32 <= row_end;
       const int half = t.nw / 2, c_lo = ((warp - 2) / 4) * half;
       if (t.nkb > 0) {
         const bool ready = mbar_wait_cluster(tfull0 + 8 * acc, acc_phase, &abort_flag, p.status);
@@ -694,30 +702,51 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * BN);
+      if (RAGGED_K) {
+        // dW's rows end with its tensor, where the TMA store clips them.
 #pragma unroll 1
-      for (int c = c_lo; c < c_lo + half; c += 32) {
-        float v[32];
-        if (t.nkb > 0) {
-          tmem_ld32(taddr + c, v);
-        } else {
+        for (int c = c_lo; c < c_lo + half; c += 64) {
+          const int col = t.n0 + c;
+          if (col >= pr.N || wrow0 >= pr.M) break;
+          float v[2][32];
+          if (t.nkb > 0) {
+            tmem_ld32(taddr + c, v[0]);
+            tmem_ld32(taddr + c + 32, v[1]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-        const int col = t.n0 + c;
-        if (col >= pr.N) continue;
-        if (tma) {
-          stage_begin<NS>(lane);
+            for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0.f;
+          }
+          stage_begin(lane);
           stage_row(v, stg, lane);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (RAGGED_K) tma_store_3d(&tm.o[t.pi], col, wrow0, t.g, stg);
-            else tma_store_2d(&tm.o[t.pi], col, wrow0, stg);
+            tma_store_3d(&tm.o[t.pi], col, wrow0, t.g, stg);
             bulk_commit();
           }
-          if (NS > 1) stg = stg == stg0 ? stg0 + kStgBytes : stg0;
-        } else if (row < row_end) {
-          store_row(pr.out + (size_t)row * pr.N + col, v, pr.N - col);
+        }
+      } else {
+        // dX's groups end inside the tensor: a block of rows reaching past a
+        // group's last one is stored lane by lane.
+        const bool tma = pr.tma_out && wrow0 + 32 <= t.hi;
+#pragma unroll 1
+        for (int c = c_lo; c < c_lo + half; c += 32) {
+          const int col = t.n0 + c;
+          if (col >= pr.N) break;
+          float v[32];
+          tmem_ld32(taddr + c, v);
+          if (tma) {
+            stage_begin(lane);
+            stage_row(v, stg, lane);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tm.o[t.pi], col, wrow0, stg);
+              bulk_commit();
+            }
+          } else if (row < t.hi) {
+            store_row(pr.out + (size_t)row * pr.N + col, v, pr.N - col);
+          }
         }
       }
       if (t.nkb > 0) {
@@ -740,9 +769,10 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
 }
 
 // ------------------------------------------------------------ host side
-// bf16 tensor [z, rows, cols] (z = 1: 2-D), box {bx, by}; `swizzle` 128 for
-// operands (64 columns), 64 for stored tiles (32 columns).
+// bf16 tensor [z, rows, cols] (z = 0: 2-D), box {bx, by}, swizzled by the
+// box's row: 128 bytes (64 columns) or 64 (32 columns).
 bool make_map(CUtensorMap *m, const void *ptr, int64_t cols, int64_t rows, int64_t z, int bx, int by, bool store) {
+  const bool narrow = bx == 32;
   const auto fn = tensor_map_encoder();
   if (!fn) return false;
   const int rank = z > 0 ? 3 : 2;
@@ -751,7 +781,7 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t cols, int64_t rows, int64
   cuuint32_t box[3] = {(cuuint32_t)bx, (cuuint32_t)by, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             store ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -761,14 +791,17 @@ bool operand_k(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols) {  /
 bool operand_mn(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t z) {
   return make_map(m, ptr, cols, rows, z, 64, 64, false);
 }
-bool stored(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t z) {
-  return make_map(m, ptr, cols, rows, z, 32, 32, true);
+bool stored(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols) {
+  return make_map(m, ptr, cols, rows, 0, 32, 32, true);
+}
+bool stored_grouped(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t z) {
+  return make_map(m, ptr, cols, rows, z, 64, 32, true);
 }
 
-template <auto kern, int threads, int ns, typename Maps, typename Params>
+template <auto kern, int threads, uint32_t staging, typename Maps, typename Params>
 int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cudaStream_t stream) {
   if (max_tiles == 0) return MOE_OK;
-  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(ns)));
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(staging)));
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cudaLaunchAttribute attr[1];
@@ -779,7 +812,7 @@ int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cuda
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem_bytes(ns);
+  cfg.dynamicSmemBytes = smem_bytes(staging);
   cfg.stream = stream;
   cfg.gridDim = dim3(2 * (unsigned)(num_sms() / 2));
   // Co-resident CTA pairs, asked once per kernel (a function-local static is
@@ -821,12 +854,12 @@ int run_act_grad(const MlpBwdProblem *q, int n, bool gated, int32_t *status, cud
         !operand_k(&maps.w1[k], s.W1, (int64_t)s.n_groups * h1, s.d) ||
         !operand_mn(&maps.w2[k], s.W2, s.d, s.h, s.n_groups))
       return MOE_ERR_CUDA;
-    o.tma_out = stored(&maps.H[k], s.H, s.rows, s.h, 0) && stored(&maps.dU[k], s.dU, s.rows, h1, 0);
+    o.tma_out = stored(&maps.H[k], s.H, s.rows, s.h) && stored(&maps.dU[k], s.dU, s.rows, h1);
     tiles += row_tiles(s) * div_up(s.h, gated ? BN / 2 : BN);
   }
   if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
-  return gated ? launch_pairs<act_grad_kernel<true>, kThreads, 1>(maps, pd, tiles, stream)
-               : launch_pairs<act_grad_kernel<false>, kThreads, 1>(maps, pd, tiles, stream);
+  return gated ? launch_pairs<act_grad_kernel<true>, kThreads, kStgBytes>(maps, pd, tiles, stream)
+               : launch_pairs<act_grad_kernel<false>, kThreads, kStgBytes>(maps, pd, tiles, stream);
 }
 
 }  // namespace
@@ -850,11 +883,11 @@ int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStre
     o.out = static_cast<__nv_bfloat16 *>(s.dx);
     if (!operand_k(&maps.a[k], s.dU, s.rows, h1) || !operand_mn(&maps.b[k], s.W1, h1, s.d, s.n_groups))
       return MOE_ERR_CUDA;
-    o.tma_out = stored(&maps.o[k], s.dx, s.rows, s.d, 0);
+    o.tma_out = stored(&maps.o[k], s.dx, s.rows, s.d);
     tiles += row_tiles(s) * div_up(s.d, BN);
   }
   if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
-  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>, kThreads, 1>(maps, pd, tiles, stream)) != MOE_OK) return st;
+  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>, kThreads, kStgBytes>(maps, pd, tiles, stream)) != MOE_OK) return st;
   memset(&maps, 0, sizeof(maps));
   memset(&pd, 0, sizeof(pd));
   pd.status = status;
@@ -873,12 +906,12 @@ int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStre
       const void *A = which ? s.dU : s.dy, *B = which ? s.x : s.H;
       if (s.rows > 0 && (!operand_mn(&maps.a[k], A, s.rows, o.M, 0) || !operand_mn(&maps.b[k], B, s.rows, o.N, 0)))
         return MOE_ERR_CUDA;
-      if (!stored(&maps.o[k], out, o.M, o.N, s.n_groups)) return MOE_ERR_CUDA;
+      if (!stored_grouped(&maps.o[k], out, o.M, o.N, s.n_groups)) return MOE_ERR_CUDA;
       tiles += s.n_groups * div_up(o.M, BMP) * div_up(o.N, BN);
       if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
       o.tile_end = (int)tiles;
     }
-  return launch_pairs<mlp_bwd_pair_kernel<true>, kThreads + 32, staging_tiles(true)>(maps, pd, tiles, stream);
+  return launch_pairs<mlp_bwd_pair_kernel<true>, kThreads + 32, staging_bytes(true)>(maps, pd, tiles, stream);
 }
 
 }  // namespace moe
