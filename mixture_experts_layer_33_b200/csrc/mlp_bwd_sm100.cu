@@ -143,6 +143,29 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float (&v)[32]
     }
 }
 
+// 64 consecutive fp32 columns of this thread's TMEM lane, both loads in flight.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[2][32]) {
+  uint32_t r[2][32];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[h][0]), "=r"(r[h][1]), "=r"(r[h][2]), "=r"(r[h][3]), "=r"(r[h][4]), "=r"(r[h][5]), "=r"(r[h][6]),
+          "=r"(r[h][7]), "=r"(r[h][8]), "=r"(r[h][9]), "=r"(r[h][10]), "=r"(r[h][11]), "=r"(r[h][12]),
+          "=r"(r[h][13]), "=r"(r[h][14]), "=r"(r[h][15]), "=r"(r[h][16]), "=r"(r[h][17]), "=r"(r[h][18]),
+          "=r"(r[h][19]), "=r"(r[h][20]), "=r"(r[h][21]), "=r"(r[h][22]), "=r"(r[h][23]), "=r"(r[h][24]),
+          "=r"(r[h][25]), "=r"(r[h][26]), "=r"(r[h][27]), "=r"(r[h][28]), "=r"(r[h][29]), "=r"(r[h][30]),
+          "=r"(r[h][31])
+        : "r"(taddr + 32 * h));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[h][i] = __uint_as_float(r[h][i]);
+}
+
 // H = GELU(u) and GELU'(u) of two values. With Q = 1 - Phi(|u|) =
 // 0.5 P(t) exp(-u^2/2) (Abramowitz & Stegun 7.1.26, as in gelu_erf_x2; the
 // error in Phi is below 1e-7) the exponential serves both:
@@ -479,7 +502,8 @@ template <> struct Tiles<false> {
 };
 template <> struct Tiles<true> {
   int t, step;
-  __device__ void init(const Sched *, const GemmParams &, int id, int n) { t = id; step = n; }
+  const int *rows;  // the groups' row offsets in shared memory
+  __device__ void init(const int *offsets, const GemmParams &, int id, int n) { t = id; step = n; rows = offsets; }
   __device__ bool next(const GemmParams &p, Tile &o) {
     int pi = 0, first = 0;
     while (pi < p.n_probs && t >= p.pr[pi].tile_end) first = p.pr[pi++].tile_end;
@@ -492,8 +516,8 @@ template <> struct Tiles<true> {
     o.m0 = (r / ntn) * BMP;
     o.n0 = (r % ntn) * BN;
     o.nw = pr.N - o.n0 <= BN / 2 ? BN / 2 : BN;
-    o.lo = pr.offsets ? pr.offsets[o.g] : 0;
-    o.hi = pr.offsets ? pr.offsets[o.g + 1] : (int)pr.rows;
+    o.lo = pr.offsets ? rows[o.g] : 0;
+    o.hi = pr.offsets ? rows[o.g + 1] : (int)pr.rows;
     check_group_rows(o.lo, o.hi, pr.rows, p.status);
     o.nkb = (o.hi - o.lo + BK - 1) / BK;
     t += step;
@@ -516,8 +540,9 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   __shared__ __align__(8) uint64_t bars[4 * STAGES + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ typename std::conditional<RAGGED_K, char, Sched>::type sched_mem;
-  Sched *sched = reinterpret_cast<Sched *>(&sched_mem);  // dX only
+  // dX: the table of row tiles; dW: the routed groups' row offsets.
+  struct Offsets { int at[kMaxLayerExperts + 1]; };
+  __shared__ typename std::conditional<RAGGED_K, Offsets, Sched>::type table;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -553,12 +578,19 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  if (!RAGGED_K && warp == 2) {
-    int run = 0, ne = 0;
-    for (int pi = 0; pi < p.n_probs; ++pi)
-      sched_add(*sched, pi, p.pr[pi].offsets, p.pr[pi].n_groups, p.pr[pi].rows, BMP, (p.pr[pi].N + BN - 1) / BN,
-                p.status, run, ne);
-    sched_close(*sched, p.n_probs, run, ne);
+  if (warp == 2) {
+    if constexpr (RAGGED_K) {
+      // Every problem with offsets has the routed experts' ones.
+      for (int pi = 0; pi < p.n_probs; ++pi)
+        if (p.pr[pi].offsets)
+          for (int g = lane; g <= p.pr[pi].n_groups; g += 32) table.at[g] = p.pr[pi].offsets[g];
+    } else {
+      int run = 0, ne = 0;
+      for (int pi = 0; pi < p.n_probs; ++pi)
+        sched_add(table, pi, p.pr[pi].offsets, p.pr[pi].n_groups, p.pr[pi].rows, BMP, (p.pr[pi].N + BN - 1) / BN,
+                  p.status, run, ne);
+      sched_close(table, p.n_probs, run, ne);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -566,7 +598,8 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   Tiles<RAGGED_K> tiles;  // the same in both CTAs of the pair
-  tiles.init(sched, p, (int)cluster_id_x(), (int)nclusters_x());
+  if constexpr (RAGGED_K) tiles.init(table.at, p, (int)cluster_id_x(), (int)nclusters_x());
+  else tiles.init(&table, p, (int)cluster_id_x(), (int)nclusters_x());
   const uint32_t leader_full0 = mapa_shared(full0, 0), leader_tempty0 = mapa_shared(tempty0, 0);
   Tile t;
 
@@ -710,8 +743,7 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
           if (col >= pr.N || wrow0 >= pr.M) break;
           float v[2][32];
           if (t.nkb > 0) {
-            tmem_ld32(taddr + c, v[0]);
-            tmem_ld32(taddr + c + 32, v[1]);
+            tmem_ld64(taddr + c, v);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0.f;
