@@ -14,13 +14,18 @@
 //   dpre_gamma = sum_b (1 + scale_b) S1_b, dpre_beta = sum_b (1 + scale_b) S0_b,
 //   dpost_gamma = sum_b gate_b P_b.
 //
-// Bound by HBM: each row is read and written once and stays in registers
-// between the statistics, so a CTA takes whole rows (a thread owns 8 NV
-// columns) and R rows at a time, which puts R loads per operand in flight
-// and shares one block reduction between R rows. Variances are sums of
-// squares of centred values (two reductions), not differences of moments:
-// with a mean of 100 standard deviations the latter would lose 4 digits.
-// Everything between the loads and the stores is fp32.
+// Bound by HBM, and close behind it by instruction issue: each row is read
+// and written once and stays in registers between the statistics. A CTA takes
+// whole rows, a thread 8 columns of them (16-byte accesses), and several rows
+// at a time, whose block reductions share their barriers; the factors and the
+// column sums of a thread's columns stay in its registers over all rows of a
+// condition row. A warp per row needs no barriers, but a lane then holds 36
+// and more columns: too few warps fit an SM to hide their latencies
+// (8192 x 1152, LayerNorm: forward 24 us, backward 50-55 us).
+// Variances are sums of squares of centred values (two reductions), not
+// differences of moments: with a mean of 100 standard deviations the latter
+// would lose 4 digits. Everything between the loads and the stores is fp32,
+// most of it on packed pairs.
 #include "backward.h"
 
 namespace moe {
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(BlockNormArgs a) {
       for (int i = 0; i < R; ++i) {
         const bool live = col[q] && s0 + i < a.T;
         float gt[8];
-        load_or(gate, (size_t)((s0 + i) / a.group) * a.cond_stride + c[q], live, 1.f, gt);
+        load_or(gate, (size_t)((uint32_t)(s0 + i) / (uint32_t)a.group) * a.cond_stride + c[q], live, 1.f, gt);
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[i][q][j] = fmaf(a.res_scale, xr[i][q][j], gt[j] * (u[i][q][j] * pg[j]));
         if (y && live) store8(y + (size_t)(s0 + i) * a.d + c[q], u[i][q]);
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(BlockNormArgs a) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (!(col[q] && s0 + i < a.T)) continue;
-        const size_t at = (size_t)((s0 + i) / a.group) * a.cond_stride + c[q];
+        const size_t at = (size_t)((uint32_t)(s0 + i) / (uint32_t)a.group) * a.cond_stride + c[q];
         float sc[8], sh[8];
         load_or(scale, at, true, 0.f, sc);
         load_or(shift, at, true, 0.f, sh);
@@ -203,36 +208,483 @@ __global__ void __launch_bounds__(512) block_norm_kernel(BlockNormArgs a) {
 
 // The rows are cut into segments of seg_len consecutive tokens of one
 // condition row (per_group segments each), a contiguous range of segments to
-// a CTA. A segment that is its whole group writes that row's condition
-// gradients itself; otherwise its sums go to part [segment][3][d]. The CTA's
-// sums for the weights go to wpart [cta][3][d] when they are wanted. A second
-// launch adds both up in order.
-struct NormBwdPlan {
+// a CTA.
+struct NormPlan {
   int group, per_group, seg_len, grid;
   int64_t groups, segments;
 };
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kBwdCtas = 148 * 4;
-
 // `conds`: rows of one group share conditions, so they belong together; else
-// the whole input is one group. `rows`: tokens a CTA takes at a time.
-NormBwdPlan norm_bwd_plan(int T, int group, bool conds, int rows) {
-  NormBwdPlan p;
+// the whole input is one group. `rows`: tokens a CTA takes at a time, `ctas`:
+// those that run at once. With fewer groups than CTAs each group is cut into
+// as many segments as still run at once.
+NormPlan norm_plan(int T, int group, bool conds, int rows, int ctas) {
+  NormPlan p;
   p.group = conds && group < T ? group : (T > 0 ? T : 1);
   p.groups = ceil_div(T, p.group);
-  const int64_t want = ceil_div(ceil_div(T > 0 ? T : 1, kBwdCtas), rows) * rows;
-  p.per_group = (int)ceil_div(p.group, want);
-  p.seg_len = (int)(ceil_div(ceil_div(p.group, p.per_group), rows) * rows);
+  const int64_t cut = p.groups > 0 && p.groups < ctas ? ctas / p.groups : 1;
+  p.seg_len = (int)(ceil_div(ceil_div(p.group, cut), rows) * rows);
   p.per_group = (int)ceil_div(p.group, p.seg_len);
   p.segments = p.groups * p.per_group;
-  p.grid = (int)(p.segments < kBwdCtas ? p.segments : kBwdCtas);
+  p.grid = (int)(p.segments < ctas ? p.segments : ctas);
   return p;
 }
+struct Segment {
+  int64_t group;
+  int lo, hi;  // tokens
+};
+__device__ __forceinline__ Segment segment_of(const NormPlan &p, int64_t seg, int T) {
+  Segment s;
+  s.group = seg / p.per_group;
+  const int64_t lo = s.group * p.group + (seg - s.group * p.per_group) * p.seg_len;
+  int64_t hi = lo + p.seg_len;
+  if (hi > (s.group + 1) * p.group) hi = (s.group + 1) * p.group;
+  if (hi > T) hi = T;
+  s.lo = (int)(lo < T ? lo : T);
+  s.hi = (int)hi;
+  return s;
+}
 
-template <typename T, int NV, int R>
-__global__ void __launch_bounds__(512) block_norm_bwd_kernel(BlockNormArgs a, NormBwdPlan p, float *part,
+// ---- many rows of up to 4096 columns: a thread owns 8 of them
+//
+// 8 fp32 columns as packed pairs.
+struct V8 {
+  uint64_t v[4];
+  __device__ __forceinline__ void fill(float f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_splat(f);
+  }
+};
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float f2_sum(uint64_t a) {
+  float lo, hi;
+  f2_unpack(a, lo, hi);
+  return lo + hi;
+}
+// 8 columns as loaded. Kept apart from their conversion so that the loads of
+// all rows and operands are issued before the first is waited for.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool live) {
+    u = make_uint4(0, 0, 0, 0);
+    if (live) u = *reinterpret_cast<const uint4 *>(p);
+  }
+  __device__ __forceinline__ V8 get() const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // a bf16 is the upper half of its fp32
+      r.v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    return r;
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p, bool live) {
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      a = *reinterpret_cast<const float4 *>(p);
+      b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+  }
+  __device__ __forceinline__ V8 get() const {
+    V8 r;
+    r.v[0] = f2_pack(a.x, a.y);
+    r.v[1] = f2_pack(a.z, a.w);
+    r.v[2] = f2_pack(b.x, b.y);
+    r.v[3] = f2_pack(b.z, b.w);
+    return r;
+  }
+};
+template <typename T>
+__device__ __forceinline__ V8 load_v8(const T *p) {
+  Raw8<T> r;
+  r.load(p, true);
+  return r.get();
+}
+template <typename T>
+__device__ __forceinline__ void store_v8(T *p, const V8 &a) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(a.v[i], f[2 * i], f[2 * i + 1]);
+  store8(p, f);
+}
+__device__ __forceinline__ float sum_v8(const V8 &a) {
+  return f2_sum(f2_add(f2_add(a.v[0], a.v[1]), f2_add(a.v[2], a.v[3])));
+}
+__device__ __forceinline__ float dot_v8(const V8 &a, const V8 &b) {
+  uint64_t s = f2_mul(a.v[0], b.v[0]), t = f2_mul(a.v[1], b.v[1]);
+  s = f2_fma(a.v[2], b.v[2], s);
+  t = f2_fma(a.v[3], b.v[3], t);
+  return f2_sum(f2_add(s, t));
+}
+// `f` past the row's end (no thread's columns cross it: d is a multiple of 8).
+template <typename T>
+__device__ __forceinline__ V8 load_v8_or(const T *p, size_t i, bool live, float f) {
+  if (p && live) return load_v8(p + i);
+  V8 r;
+  r.fill(f);
+  return r;
+}
+
+// Block-wide sums of K = 4 or 8 values, the same in every thread. Halving
+// exchanges leave each lane one value to finish (9 shuffles for 8 values
+// instead of 40). `buf` holds two buffers used in turn, as above.
+constexpr int kVecWarps = 16;
+struct VecReducer {
+  float *buf;  // [2][kVecWarps][8]
+  int turn;
+};
+template <int K>
+__device__ __forceinline__ void block_sum_vec(float (&v)[K], VecReducer &red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  float k[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) k[i] = v[i];
+  int idx = 0;
+#pragma unroll
+  for (int n = K / 2, o = 16; n >= 1; n /= 2, o /= 2) {
+    const bool up = (lane & o) != 0;  // this lane keeps the upper half of the values
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? k[i] : k[i + n], keep = up ? k[i + n] : k[i];
+      k[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+    idx = 2 * idx + (up ? 1 : 0);
+  }
+  constexpr int kRest = 32 / K;  // lanes that share a value
+#pragma unroll
+  for (int o = kRest / 2; o > 0; o >>= 1) k[0] += __shfl_xor_sync(0xffffffffu, k[0], o);
+  float *b = red.buf + red.turn * kVecWarps * 8;
+  red.turn ^= 1;
+  if ((lane & (kRest - 1)) == 0) b[warp * 8 + idx] = k[0];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = 0.f;
+  for (int w = 0; w < nw; ++w) {
+#pragma unroll
+    for (int i = 0; i < K; i += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(b + w * 8 + i);
+      v[i] += f.x;
+      v[i + 1] += f.y;
+      v[i + 2] += f.z;
+      v[i + 3] += f.w;
+    }
+  }
+}
+
+// A segment's conditions and weights are folded into three factors per
+// column, fg = gate post_gamma, fs = (1 + scale) pre_gamma, fb = (1 + scale)
+// pre_beta + shift: y = res_scale x + fg N(h), z = fs N(y) + fb.
+constexpr int kFwdRows = 4;
+template <typename T>
+__global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, NormPlan p) {
+  constexpr int R = kFwdRows;
+  __shared__ __align__(16) float red_buf[2 * kVecWarps * 8];
+  VecReducer red{red_buf, 0};
+  const T *h = static_cast<const T *>(a.h), *x = static_cast<const T *>(a.x);  // either may be y
+  T *y = static_cast<T *>(a.y), *z = static_cast<T *>(a.z);
+  const int c = threadIdx.x * 8;
+  const bool col = c < a.d;
+  const float inv_d = 1.0f / (float)a.d;
+  const uint64_t alpha = f2_splat(a.res_scale);
+  const int64_t g_lo = p.segments * blockIdx.x / p.grid, g_hi = p.segments * (blockIdx.x + 1) / p.grid;
+  // v less its mean, and the rows' scales; columns past d stay 0.
+  auto centre = [&](V8 (&v)[R], float (&r)[R], int kind) {
+    float s[R];
+    if (kind == MOE_NORM_LAYER) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) s[i] = sum_v8(v[i]);
+      block_sum_vec(s, red);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint64_t m = f2_splat(col ? -s[i] * inv_d : 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i].v[j] = f2_add(v[i].v[j], m);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) s[i] = dot_v8(v[i], v[i]);
+    block_sum_vec(s, red);
+#pragma unroll
+    for (int i = 0; i < R; ++i) r[i] = 1.0f / sqrtf(fmaf(s[i], inv_d, a.eps));
+  };
+  for (int64_t seg = g_lo; seg < g_hi; ++seg) {
+    const Segment sg = segment_of(p, seg, a.T);
+    const size_t cond = (size_t)sg.group * a.cond_stride + c;
+    V8 fg = load_v8_or(static_cast<const T *>(a.gate), cond, col, 1.f);
+    V8 fs = load_v8_or(static_cast<const T *>(a.scale), cond, col, 0.f);
+    V8 fb = load_v8_or(static_cast<const T *>(a.shift), cond, col, 0.f);
+    {
+      const V8 po = load_v8_or(static_cast<const T *>(a.post_gamma), c, col, 1.f);
+      const V8 pg = load_v8_or(static_cast<const T *>(a.pre_gamma), c, col, 1.f);
+      const V8 pb = load_v8_or(static_cast<const T *>(a.pre_beta), c, col, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t s1 = f2_add(fs.v[j], f2_splat(1.f));
+        fg.v[j] = f2_mul(fg.v[j], po.v[j]);
+        fb.v[j] = f2_fma(s1, pb.v[j], fb.v[j]);
+        fs.v[j] = f2_mul(s1, pg.v[j]);
+      }
+    }
+    for (int s0 = sg.lo; s0 < sg.hi; s0 += R) {
+      Raw8<T> rh[R], rx[R];
+      V8 u[R];
+      float r[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const bool live = col && s0 + i < sg.hi;
+        const size_t at = (size_t)(s0 + i) * a.d + c;
+        rh[i].load(h + at, live && h);
+        rx[i].load(x + at, live && x);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        u[i] = rh[i].get();
+        r[i] = 1.f;
+      }
+      if (h && a.post != MOE_NORM_NONE) centre(u, r, a.post);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint64_t rr = f2_splat(r[i]);
+        const V8 xv = rx[i].get();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t t = f2_mul(f2_mul(u[i].v[j], rr), fg.v[j]);
+          u[i].v[j] = f2_fma(alpha, xv.v[j], t);
+        }
+        if (y && col && s0 + i < sg.hi) store_v8(y + (size_t)(s0 + i) * a.d + c, u[i]);
+      }
+      if (!z) continue;
+      centre(u, r, a.pre);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (!(col && s0 + i < sg.hi)) continue;
+        const uint64_t rr = f2_splat(r[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[i].v[j] = f2_fma(f2_mul(u[i].v[j], rr), fs.v[j], fb.v[j]);
+        store_v8(z + (size_t)(s0 + i) * a.d + c, u[i]);
+      }
+    }
+  }
+}
+
+// The gradient, two rows at a time. With yc = y - mean(y), n = r yc and
+// g = dz (1 + scale) pre_gamma:
+//   t = dy + r (g - mean(g)) - r^3 mean(g yc) yc
+// so that mean(y) and mean(g), then mean(yc^2) and mean(g yc), and the same
+// of h, each take one reduction. Sums of a segment as in the other kernels;
+// the CTA's sums for the weights are kept in wpart, which only it touches.
+constexpr int kBwdRows = 2;
+template <typename T, bool POST>
+__global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a, NormPlan p, float *part,
+                                                                 float *wpart) {
+  constexpr int R = kBwdRows;
+  __shared__ __align__(16) float red_buf[2 * kVecWarps * 8];
+  VecReducer red{red_buf, 0};
+  const T *h = static_cast<const T *>(a.h), *y = static_cast<const T *>(a.yin);
+  const T *dz = static_cast<const T *>(a.dz), *dy = static_cast<const T *>(a.dy);  // either may be dh or dx
+  T *dh = static_cast<T *>(a.dh), *dx = static_cast<T *>(a.dx);
+  const bool want_h = dh || a.dgate || a.dpost_gamma;
+  const bool pre_mean = a.pre == MOE_NORM_LAYER, post_mean = a.post == MOE_NORM_LAYER;
+  const int c = threadIdx.x * 8;
+  const bool col = c < a.d;
+  const float inv_d = 1.0f / (float)a.d;
+  const uint64_t alpha = f2_splat(a.res_scale);
+  const int64_t g_lo = p.segments * blockIdx.x / p.grid, g_hi = p.segments * (blockIdx.x + 1) / p.grid;
+  for (int64_t seg = g_lo; seg < g_hi; ++seg) {
+    const Segment sg = segment_of(p, seg, a.T);
+    const size_t cond = (size_t)sg.group * a.cond_stride + c;
+    V8 fz = load_v8_or(static_cast<const T *>(a.scale), cond, col, 0.f);
+    V8 fh = load_v8_or(static_cast<const T *>(a.gate), cond, col, 1.f);
+    V8 S0, S1, P;
+    S0.fill(0.f);
+    S1.fill(0.f);
+    P.fill(0.f);
+    {
+      // Factors past the row's end are 0: nothing there enters a mean.
+      const V8 pg = load_v8_or(static_cast<const T *>(a.pre_gamma), c, col, col ? 1.f : 0.f);
+      const V8 po = load_v8_or(static_cast<const T *>(a.post_gamma), c, col, col ? 1.f : 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        fz.v[j] = f2_mul(f2_add(fz.v[j], f2_splat(1.f)), pg.v[j]);
+        fh.v[j] = f2_mul(fh.v[j], po.v[j]);
+      }
+    }
+    for (int s0 = sg.lo; s0 < sg.hi; s0 += R) {
+      Raw8<T> rn[R], rz[R], rt[R], rm[R];
+      V8 t[R], m[R], n[R], g[R];
+      float rh[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const bool live = col && s0 + i < sg.hi;
+        const size_t at = (size_t)(s0 + i) * a.d + c;
+        rn[i].load(y + at, live && dz);
+        rz[i].load(dz + at, live && dz);
+        rm[i].load(h + at, live && want_h && h);
+        rt[i].load(dy + at, live && dy);
+        rh[i] = 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        n[i] = rn[i].get();
+        g[i] = rz[i].get();
+        m[i] = rm[i].get();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          S0.v[j] = f2_add(S0.v[j], g[i].v[j]);
+          g[i].v[j] = f2_mul(g[i].v[j], fz.v[j]);
+        }
+      }
+      constexpr int K = POST ? 8 : 4;
+      float s[K], mg[R];
+#pragma unroll
+      for (int i = 0; i < K; ++i) s[i] = 0.f;
+      if (pre_mean || (POST && post_mean)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          s[i] = sum_v8(n[i]);
+          s[R + i] = sum_v8(g[i]);
+          if (POST) s[2 * R + i] = sum_v8(m[i]);
+        }
+        block_sum_vec(s, red);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        mg[i] = pre_mean ? s[R + i] * inv_d : 0.f;
+        const uint64_t my = f2_splat(pre_mean && col ? -s[i] * inv_d : 0.f);
+        const uint64_t mh = f2_splat(POST && post_mean && col ? -s[POST ? 2 * R + i : 0] * inv_d : 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          n[i].v[j] = f2_add(n[i].v[j], my);
+          if (POST) m[i].v[j] = f2_add(m[i].v[j], mh);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        s[i] = dot_v8(n[i], n[i]);
+        s[R + i] = dot_v8(g[i], n[i]);
+        if (POST) s[2 * R + i] = dot_v8(m[i], m[i]);
+      }
+      block_sum_vec(s, red);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const bool live = col && s0 + i < sg.hi;
+        t[i] = rt[i].get();
+        if (dz) {
+          const V8 q = rz[i].get();
+          const float r = 1.0f / sqrtf(fmaf(s[i], inv_d, a.eps));
+          const float k = r * (s[R + i] * inv_d) * r;  // mean(g n), times r: n is r yc
+          const uint64_t rr = f2_splat(r), c0 = f2_splat(-r * mg[i]), c1 = f2_splat(-k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            n[i].v[j] = f2_mul(n[i].v[j], rr);  // n
+            S1.v[j] = f2_fma(q.v[j], n[i].v[j], S1.v[j]);
+            t[i].v[j] = f2_add(t[i].v[j], f2_fma(rr, g[i].v[j], f2_fma(c1, n[i].v[j], c0)));
+          }
+        }
+        if (dx && live) {
+          V8 o;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o.v[j] = f2_mul(alpha, t[i].v[j]);
+          store_v8(dx + (size_t)(s0 + i) * a.d + c, o);
+        }
+        if (POST) rh[i] = 1.0f / sqrtf(fmaf(s[POST ? 2 * R + i : 0], inv_d, a.eps));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (POST) m[i].v[j] = f2_mul(m[i].v[j], f2_splat(rh[i]));
+          P.v[j] = f2_fma(t[i].v[j], m[i].v[j], P.v[j]);
+          t[i].v[j] = f2_mul(t[i].v[j], fh.v[j]);
+        }
+      }
+      if (!dh) continue;
+      if (POST) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          w[i] = sum_v8(t[i]);
+          w[R + i] = dot_v8(t[i], m[i]);
+        }
+        block_sum_vec(w, red);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const uint64_t rr = f2_splat(rh[i]), c0 = f2_splat(post_mean ? -rh[i] * (w[i] * inv_d) : 0.f);
+          const uint64_t c1 = f2_splat(-rh[i] * (w[R + i] * inv_d));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[i].v[j] = f2_fma(rr, t[i].v[j], f2_fma(c1, m[i].v[j], c0));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (col && s0 + i < sg.hi) store_v8(dh + (size_t)(s0 + i) * a.d + c, t[i]);
+    }
+    if (!col) continue;
+    if (part) {
+      float *o = part + (size_t)seg * 3 * a.d + c;
+      store_v8(o, S0);
+      store_v8(o + a.d, S1);
+      store_v8(o + 2 * (size_t)a.d, P);
+    } else {
+      const size_t at = (size_t)sg.group * a.dcond_stride + c;
+      V8 o;
+      if (a.dshift) store_v8(a.dshift + at, S0);
+      if (a.dscale) {
+        const V8 pg = load_v8_or(static_cast<const T *>(a.pre_gamma), c, true, 1.f);
+        const V8 pb = load_v8_or(static_cast<const T *>(a.pre_beta), c, true, 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.v[j] = f2_fma(pg.v[j], S1.v[j], f2_mul(pb.v[j], S0.v[j]));
+        store_v8(a.dscale + at, o);
+      }
+      if (a.dgate) {
+        const V8 po = load_v8_or(static_cast<const T *>(a.post_gamma), c, true, 1.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.v[j] = f2_mul(po.v[j], P.v[j]);
+        store_v8(a.dgate + at, o);
+      }
+    }
+    if (wpart) {
+      float *o = wpart + (size_t)blockIdx.x * 3 * a.d + c;
+      const V8 sc = load_v8_or(static_cast<const T *>(a.scale), cond, true, 0.f);
+      const V8 gt = load_v8_or(static_cast<const T *>(a.gate), cond, true, 1.f);
+      V8 w0, w1, w2;
+      w0.fill(0.f);
+      w1.fill(0.f);
+      w2.fill(0.f);
+      if (seg > g_lo) {
+        w0 = load_v8(o);
+        w1 = load_v8(o + a.d);
+        w2 = load_v8(o + 2 * (size_t)a.d);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t s1 = f2_add(sc.v[j], f2_splat(1.f));
+        w0.v[j] = f2_fma(s1, S1.v[j], w0.v[j]);
+        w1.v[j] = f2_fma(s1, S0.v[j], w1.v[j]);
+        w2.v[j] = f2_fma(gt.v[j], P.v[j], w2.v[j]);
+      }
+      store_v8(o, w0);
+      store_v8(o + a.d, w1);
+      store_v8(o + 2 * (size_t)a.d, w2);
+    }
+  }
+}
+
+// ---- gradient of wide rows
+//
+// A segment that is its whole group writes that row's condition gradients
+// itself; otherwise its sums go to part [segment][3][d]. The CTA's sums for
+// the weights go to wpart [cta][3][d] when they are wanted. A second launch
+// adds both up in order.
+template <typename T>
+__global__ void __launch_bounds__(512) block_norm_bwd_kernel(BlockNormArgs a, NormPlan p, float *part,
                                                              float *wpart) {
+  constexpr int NV = 2, R = 1;
   __shared__ float red_buf[2 * kMaxWarps * 2 * R];
   const T *h = static_cast<const T *>(a.h), *y = static_cast<const T *>(a.yin);
   const T *dz = static_cast<const T *>(a.dz), *dy = static_cast<const T *>(a.dy);  // either may be dh or dx
@@ -399,12 +851,13 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(BlockNormArgs a, No
 
 // Sums the partial blocks in order: blockIdx.y < groups adds a group's
 // segments into its condition gradients, the next one the CTAs' sums into
-// the weights' gradients. 32 columns by 8 slices of the list per CTA.
+// the weights' gradients. 32 columns by kSlices slices of the list per CTA.
+constexpr int kSlices = 16;
 template <typename T>
-__global__ void __launch_bounds__(256) block_norm_sum_kernel(BlockNormArgs a, const float *part, const float *wpart,
+__global__ void __launch_bounds__(32 * kSlices) block_norm_sum_kernel(BlockNormArgs a, const float *part, const float *wpart,
                                                              int64_t first_task, int64_t groups, int per_group,
                                                              int ctas) {
-  __shared__ float sh[3][8][33];
+  __shared__ float sh[3][kSlices][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t task = first_task + blockIdx.y;
   const bool cond = part && task < groups;
@@ -413,7 +866,7 @@ __global__ void __launch_bounds__(256) block_norm_sum_kernel(BlockNormArgs a, co
   const int col = blockIdx.x * 32 + lane;
   float v[3] = {0.f, 0.f, 0.f};
   if (col < a.d) {
-    const int lo = (int)((int64_t)n * slice / 8), hi = (int)((int64_t)n * (slice + 1) / 8);
+    const int lo = (int)((int64_t)n * slice / kSlices), hi = (int)((int64_t)n * (slice + 1) / kSlices);
 #pragma unroll 4
     for (int k = lo; k < hi; ++k)
 #pragma unroll
@@ -427,7 +880,7 @@ __global__ void __launch_bounds__(256) block_norm_sum_kernel(BlockNormArgs a, co
   for (int w = 0; w < 3; ++w) {
     v[w] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[w] += sh[w][k][lane];
+    for (int k = 0; k < kSlices; ++k) v[w] += sh[w][k][lane];
   }
   if (cond) {
     const size_t at = (size_t)task * a.dcond_stride + col;
@@ -452,7 +905,11 @@ int row_threads(int d, int nv) {
 // rows take 2 vectors per thread and one row at a time (the backward spills
 // there: 12 arrays of 16 columns do not fit 128 registers).
 inline bool narrow(int d) { return d <= 4096; }
-constexpr int kFwdRows = 2, kBwdRows = 2;
+// CTAs per SM of the kernels for many rows (128 registers a thread).
+inline int ctas_per_sm(int d) {
+  const int n = 512 / row_threads(d, 1);
+  return n > 8 ? 8 : n;
+}
 
 template <typename T>
 int run_fwd(const BlockNormArgs &a, cudaStream_t stream) {
@@ -463,49 +920,53 @@ int run_fwd(const BlockNormArgs &a, cudaStream_t stream) {
   } else if (a.T <= 2 * sms) {  // few tokens: a CTA each
     block_norm_kernel<T, 1, 1><<<a.T, row_threads(a.d, 1), 0, stream>>>(a);
   } else {
-    const int64_t tiles = (a.T + kFwdRows - 1) / kFwdRows, cap = 16 * sms;
-    block_norm_kernel<T, 1, kFwdRows><<<(unsigned)(tiles < cap ? tiles : cap), row_threads(a.d, 1), 0, stream>>>(a);
+    const NormPlan p = norm_plan(a.T, a.group, a.gate || a.scale || a.shift, kFwdRows, (int)sms * ctas_per_sm(a.d));
+    block_norm_vec_kernel<T><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p);
   }
   return last_launch_status();
+}
+
+// Rows at a time and CTAs at once of the backward.
+NormPlan bwd_plan(int T, int d, int group, bool conds) {
+  const int rows = narrow(d) ? kBwdRows : 1;
+  return norm_plan(T, group, conds, rows, 148 * (narrow(d) ? ctas_per_sm(d) : 1));
 }
 
 template <typename T>
 int run_bwd(const BlockNormArgs &a, cudaStream_t stream) {
   const bool conds = a.gate || a.scale || a.dgate || a.dscale || a.dshift;
-  const int rows = narrow(a.d) && a.group >= kBwdRows ? kBwdRows : 1;
-  const NormBwdPlan p = norm_bwd_plan(a.T, a.group, conds, rows);
+  const NormPlan p = bwd_plan(a.T, a.d, a.group, conds);
   const bool cond_out = a.dgate || a.dscale || a.dshift;
   float *part = cond_out && p.per_group > 1 ? a.part : nullptr;
   float *wpart = a.dpre_gamma || a.dpre_beta || a.dpost_gamma
                      ? a.part + (part ? (size_t)p.segments * 3 * a.d : 0) : nullptr;
   if (a.T > 0) {
     if (!narrow(a.d))
-      block_norm_bwd_kernel<T, 2, 1><<<p.grid, row_threads(a.d, 2), 0, stream>>>(a, p, part, wpart);
-    else if (rows == 1)
-      block_norm_bwd_kernel<T, 1, 1><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p, part, wpart);
+      block_norm_bwd_kernel<T><<<p.grid, row_threads(a.d, 2), 0, stream>>>(a, p, part, wpart);
+    else if (a.post == MOE_NORM_NONE)
+      block_norm_bwd_vec_kernel<T, false><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p, part, wpart);
     else
-      block_norm_bwd_kernel<T, 1, kBwdRows><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p, part, wpart);
+      block_norm_bwd_vec_kernel<T, true><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p, part, wpart);
   }
   const int64_t first = part ? 0 : p.groups, last = p.groups + (wpart ? 1 : 0);
   for (int64_t t = first; t < last; t += 65535) {
     const unsigned n = (unsigned)(last - t < 65535 ? last - t : 65535);
-    block_norm_sum_kernel<T><<<dim3((a.d + 31) / 32, n), 256, 0, stream>>>(a, part, wpart, t, p.groups, p.per_group,
-                                                                          a.T > 0 ? p.grid : 0);
+    block_norm_sum_kernel<T><<<dim3((a.d + 31) / 32, n), 32 * kSlices, 0, stream>>>(a, part, wpart, t, p.groups,
+                                                                                   p.per_group, a.T > 0 ? p.grid : 0);
   }
   return last_launch_status();
 }
 
 }  // namespace
 
-// Partial sums of every way the backward can cut the rows.
+// Partial sums of either way (with or without conditions) the backward can cut the rows.
 size_t block_norm_workspace_bytes(int T, int d, int group) {
   int64_t most = 0;
-  for (int rows = 1; rows <= kBwdRows; rows += kBwdRows - 1)
-    for (int conds = 0; conds < 2; ++conds) {
-      const NormBwdPlan p = norm_bwd_plan(T, group, conds != 0, rows);
-      const int64_t n = (p.per_group > 1 ? p.segments : 0) + p.grid;
-      if (n > most) most = n;
-    }
+  for (int conds = 0; conds < 2; ++conds) {
+    const NormPlan p = bwd_plan(T, d, group, conds != 0);
+    const int64_t n = (p.per_group > 1 ? p.segments : 0) + p.grid;
+    if (n > most) most = n;
+  }
   return (size_t)most * 3 * d * 4;
 }
 
