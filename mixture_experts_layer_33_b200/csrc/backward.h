@@ -93,7 +93,7 @@ struct BlockNormArgs {
   float *part;  // workspace of block_norm_workspace_bytes()
 };
 constexpr int kNormMaxWidth = 8192;
-size_t block_norm_workspace_bytes(int T, int d, int group);
+size_t block_norm_workspace_bytes(int T, int d, int group, int dtype);
 int launch_block_norm(const BlockNormArgs &a, int dtype, cudaStream_t stream);
 int launch_block_norm_bwd(const BlockNormArgs &a, int dtype, cudaStream_t stream);
 

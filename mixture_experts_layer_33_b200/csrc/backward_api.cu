@@ -231,7 +231,7 @@ int moe_block_norm_workspace_size(const moe_norm_config *cfg, size_t *bytes) {
   const int st = check_norm(cfg);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = kAlign + align_up(block_norm_workspace_bytes(cfg->T, cfg->d, norm_group(*cfg)));
+  *bytes = kAlign + align_up(block_norm_workspace_bytes(cfg->T, cfg->d, norm_group(*cfg), cfg->dtype));
   return MOE_OK;
 }
 

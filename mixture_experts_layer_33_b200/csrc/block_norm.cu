@@ -266,48 +266,55 @@ __device__ __forceinline__ float f2_sum(uint64_t a) {
   f2_unpack(a, lo, hi);
   return lo + hi;
 }
-// 8 columns as loaded. Kept apart from their conversion so that the loads of
-// all rows and operands are issued before the first is waited for.
-template <typename T> struct Raw8;
-template <> struct Raw8<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool live) {
-    u = make_uint4(0, 0, 0, 0);
-    if (live) u = *reinterpret_cast<const uint4 *>(p);
-  }
-  __device__ __forceinline__ V8 get() const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    V8 r;
+__device__ __forceinline__ V8 unpack_v8(const __nv_bfloat16 *p) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  V8 r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // a bf16 is the upper half of its fp32
-      r.v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-    return r;
-  }
-};
-template <> struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p, bool live) {
-    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-      a = *reinterpret_cast<const float4 *>(p);
-      b = *reinterpret_cast<const float4 *>(p + 4);
-    }
-  }
-  __device__ __forceinline__ V8 get() const {
-    V8 r;
-    r.v[0] = f2_pack(a.x, a.y);
-    r.v[1] = f2_pack(a.z, a.w);
-    r.v[2] = f2_pack(b.x, b.y);
-    r.v[3] = f2_pack(b.z, b.w);
-    return r;
-  }
-};
-template <typename T>
-__device__ __forceinline__ V8 load_v8(const T *p) {
-  Raw8<T> r;
-  r.load(p, true);
-  return r.get();
+  for (int i = 0; i < 4; ++i)  // a bf16 is the upper half of its fp32
+    r.v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return r;
 }
+__device__ __forceinline__ V8 unpack_v8(const float *p) {
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+  V8 r;
+  r.v[0] = f2_pack(a.x, a.y);
+  r.v[1] = f2_pack(a.z, a.w);
+  r.v[2] = f2_pack(b.x, b.y);
+  r.v[3] = f2_pack(b.z, b.w);
+  return r;
+}
+// This thread's 8 columns of rows on their way: a ring of kFetch steps of N
+// vectors (rows by operands) in shared memory, filled by cp.async two steps
+// ahead. A thread reads only what it copied, so no barrier is involved.
+constexpr int kFetch = 3;
+template <typename T, int N> struct Fetch {
+  T *mine;  // [kFetch][N][blockDim.x][8], this thread's part
+  int slot;
+  __device__ __forceinline__ T *at(int step, int k) const {
+    return mine + (size_t)(step * N + k) * blockDim.x * 8;
+  }
+  // Vector k of a step; zeros unless `live`. The memory clobbers here and in
+  // wait() keep the reads of the ring on their side of the copies.
+  __device__ __forceinline__ void issue(int step, int k, const T *p, bool live) {
+    constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += PER)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(at(step, k) + i))),
+                   "l"(live ? p + i : p), "r"(live ? 16 : 0)
+                   : "memory");
+  }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Until all but the last `later` steps have arrived.
+  template <int later> __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(later) : "memory");
+  }
+  __device__ __forceinline__ void next() { slot = slot == kFetch - 1 ? 0 : slot + 1; }
+  __device__ __forceinline__ int last() const { return slot == 0 ? kFetch - 1 : slot - 1; }
+  __device__ __forceinline__ V8 get(int k) const { return unpack_v8(at(slot, k)); }
+};
+template <typename T, int N> size_t fetch_bytes(int threads) { return (size_t)kFetch * N * threads * 8 * sizeof(T); }
 template <typename T>
 __device__ __forceinline__ void store_v8(T *p, const V8 &a) {
   float f[8];
@@ -327,7 +334,7 @@ __device__ __forceinline__ float dot_v8(const V8 &a, const V8 &b) {
 // `f` past the row's end (no thread's columns cross it: d is a multiple of 8).
 template <typename T>
 __device__ __forceinline__ V8 load_v8_or(const T *p, size_t i, bool live, float f) {
-  if (p && live) return load_v8(p + i);
+  if (p && live) return unpack_v8(p + i);
   V8 r;
   r.fill(f);
   return r;
@@ -387,7 +394,9 @@ template <typename T>
 __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, NormPlan p) {
   constexpr int R = kFwdRows;
   __shared__ __align__(16) float red_buf[2 * kVecWarps * 8];
+  extern __shared__ __align__(16) uint8_t ring[];
   VecReducer red{red_buf, 0};
+  Fetch<T, 2 * R> rows{reinterpret_cast<T *>(ring) + threadIdx.x * 8, 0};
   const T *h = static_cast<const T *>(a.h), *x = static_cast<const T *>(a.x);  // either may be y
   T *y = static_cast<T *>(a.y), *z = static_cast<T *>(a.z);
   const int c = threadIdx.x * 8;
@@ -417,6 +426,21 @@ __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, No
   };
   for (int64_t seg = g_lo; seg < g_hi; ++seg) {
     const Segment sg = segment_of(p, seg, a.T);
+    // Rows s0 .. s0 + R - 1 of h and x into a step of the ring.
+    auto fetch = [&](int s0, int step) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const bool live = col && s0 + i < sg.hi;
+        const size_t at = (size_t)(s0 + i) * a.d + c;
+        rows.issue(step, 2 * i, h ? h + at : x, live && h);
+        rows.issue(step, 2 * i + 1, x ? x + at : h, live && x);
+      }
+      rows.commit();
+    };
+    rows.template wait<0>();  // the last segment's copies past its end
+    rows.slot = 0;
+    fetch(sg.lo, 0);
+    fetch(sg.lo + R, 1);
     const size_t cond = (size_t)sg.group * a.cond_stride + c;
     V8 fg = load_v8_or(static_cast<const T *>(a.gate), cond, col, 1.f);
     V8 fs = load_v8_or(static_cast<const T *>(a.scale), cond, col, 0.f);
@@ -434,26 +458,20 @@ __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, No
       }
     }
     for (int s0 = sg.lo; s0 < sg.hi; s0 += R) {
-      Raw8<T> rh[R], rx[R];
+      fetch(s0 + 2 * R, rows.last());
+      rows.template wait<2>();
       V8 u[R];
       float r[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const bool live = col && s0 + i < sg.hi;
-        const size_t at = (size_t)(s0 + i) * a.d + c;
-        rh[i].load(h + at, live && h);
-        rx[i].load(x + at, live && x);
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        u[i] = rh[i].get();
+        u[i] = rows.get(2 * i);
         r[i] = 1.f;
       }
       if (h && a.post != MOE_NORM_NONE) centre(u, r, a.post);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const uint64_t rr = f2_splat(r[i]);
-        const V8 xv = rx[i].get();
+        const V8 xv = rows.get(2 * i + 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint64_t t = f2_mul(f2_mul(u[i].v[j], rr), fg.v[j]);
@@ -461,6 +479,7 @@ __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, No
         }
         if (y && col && s0 + i < sg.hi) store_v8(y + (size_t)(s0 + i) * a.d + c, u[i]);
       }
+      rows.next();
       if (!z) continue;
       centre(u, r, a.pre);
 #pragma unroll
@@ -487,7 +506,9 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
                                                                  float *wpart) {
   constexpr int R = kBwdRows;
   __shared__ __align__(16) float red_buf[2 * kVecWarps * 8];
+  extern __shared__ __align__(16) uint8_t ring[];
   VecReducer red{red_buf, 0};
+  Fetch<T, 4 * R> rows{reinterpret_cast<T *>(ring) + threadIdx.x * 8, 0};
   const T *h = static_cast<const T *>(a.h), *y = static_cast<const T *>(a.yin);
   const T *dz = static_cast<const T *>(a.dz), *dy = static_cast<const T *>(a.dy);  // either may be dh or dx
   T *dh = static_cast<T *>(a.dh), *dx = static_cast<T *>(a.dx);
@@ -500,6 +521,25 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
   const int64_t g_lo = p.segments * blockIdx.x / p.grid, g_hi = p.segments * (blockIdx.x + 1) / p.grid;
   for (int64_t seg = g_lo; seg < g_hi; ++seg) {
     const Segment sg = segment_of(p, seg, a.T);
+    // Rows s0 .. s0 + R - 1 of y, dz, h and dy into a step of the ring. dh and
+    // dx of a row may be its dz or dy, which has been copied by then.
+    auto fetch = [&](int s0, int step) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const bool live = col && s0 + i < sg.hi;
+        const size_t at = (size_t)(s0 + i) * a.d + c;
+        const T *any = dz ? dz : dy;
+        rows.issue(step, 4 * i, dz ? y + at : any, live && dz);
+        rows.issue(step, 4 * i + 1, dz ? dz + at : any, live && dz);
+        rows.issue(step, 4 * i + 2, want_h && h ? h + at : any, live && want_h && h);
+        rows.issue(step, 4 * i + 3, dy ? dy + at : any, live && dy);
+      }
+      rows.commit();
+    };
+    rows.template wait<0>();  // the last segment's copies past its end
+    rows.slot = 0;
+    fetch(sg.lo, 0);
+    fetch(sg.lo + R, 1);
     const size_t cond = (size_t)sg.group * a.cond_stride + c;
     V8 fz = load_v8_or(static_cast<const T *>(a.scale), cond, col, 0.f);
     V8 fh = load_v8_or(static_cast<const T *>(a.gate), cond, col, 1.f);
@@ -518,24 +558,16 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
       }
     }
     for (int s0 = sg.lo; s0 < sg.hi; s0 += R) {
-      Raw8<T> rn[R], rz[R], rt[R], rm[R];
+      fetch(s0 + 2 * R, rows.last());
+      rows.template wait<2>();
       V8 t[R], m[R], n[R], g[R];
       float rh[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const bool live = col && s0 + i < sg.hi;
-        const size_t at = (size_t)(s0 + i) * a.d + c;
-        rn[i].load(y + at, live && dz);
-        rz[i].load(dz + at, live && dz);
-        rm[i].load(h + at, live && want_h && h);
-        rt[i].load(dy + at, live && dy);
         rh[i] = 1.f;
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        n[i] = rn[i].get();
-        g[i] = rz[i].get();
-        m[i] = rm[i].get();
+        n[i] = rows.get(4 * i);
+        g[i] = rows.get(4 * i + 1);
+        if (POST) m[i] = rows.get(4 * i + 2);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           S0.v[j] = f2_add(S0.v[j], g[i].v[j]);
@@ -576,9 +608,10 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const bool live = col && s0 + i < sg.hi;
-        t[i] = rt[i].get();
+        t[i] = rows.get(4 * i + 3);
+        if (!POST) m[i] = rows.get(4 * i + 2);
         if (dz) {
-          const V8 q = rz[i].get();
+          const V8 q = rows.get(4 * i + 1);
           const float r = 1.0f / sqrtf(fmaf(s[i], inv_d, a.eps));
           const float k = r * (s[R + i] * inv_d) * r;  // mean(g n), times r: n is r yc
           const uint64_t rr = f2_splat(r), c0 = f2_splat(-r * mg[i]), c1 = f2_splat(-k);
@@ -603,6 +636,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
           t[i].v[j] = f2_mul(t[i].v[j], fh.v[j]);
         }
       }
+      rows.next();
       if (!dh) continue;
       if (POST) {
         float w[4];
@@ -657,9 +691,9 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
       w1.fill(0.f);
       w2.fill(0.f);
       if (seg > g_lo) {
-        w0 = load_v8(o);
-        w1 = load_v8(o + a.d);
-        w2 = load_v8(o + 2 * (size_t)a.d);
+        w0 = unpack_v8(o);
+        w1 = unpack_v8(o + a.d);
+        w2 = unpack_v8(o + 2 * (size_t)a.d);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -901,10 +935,11 @@ int row_threads(int d, int nv) {
   const int vecs = d / 8;
   return ((vecs + nv - 1) / nv + 31) / 32 * 32;
 }
-// Up to 4096 columns a thread owns 8 of them (at most 512 threads); wider
-// rows take 2 vectors per thread and one row at a time (the backward spills
-// there: 12 arrays of 16 columns do not fit 128 registers).
-inline bool narrow(int d) { return d <= 4096; }
+// Rows of up to 8 KB take a thread per 8 columns (at most 512 threads, and
+// rings of at most 196 KB); wider ones 2 vectors per thread and one row at a
+// time (the backward spills there: 12 arrays of 16 columns do not fit 128
+// registers).
+template <typename T> inline bool narrow(int d) { return d * (int)sizeof(T) <= 8192; }
 // CTAs per SM of the kernels for many rows (128 registers a thread).
 inline int ctas_per_sm(int d) {
   const int n = 512 / row_threads(d, 1);
@@ -914,39 +949,46 @@ inline int ctas_per_sm(int d) {
 template <typename T>
 int run_fwd(const BlockNormArgs &a, cudaStream_t stream) {
   const int64_t sms = num_sms();
-  if (!narrow(a.d)) {
+  if (!narrow<T>(a.d)) {
     const int64_t grid = a.T < 4 * sms ? a.T : 4 * sms;
     block_norm_kernel<T, 2, 1><<<(unsigned)grid, row_threads(a.d, 2), 0, stream>>>(a);
   } else if (a.T <= 2 * sms) {  // few tokens: a CTA each
     block_norm_kernel<T, 1, 1><<<a.T, row_threads(a.d, 1), 0, stream>>>(a);
   } else {
     const NormPlan p = norm_plan(a.T, a.group, a.gate || a.scale || a.shift, kFwdRows, (int)sms * ctas_per_sm(a.d));
-    block_norm_vec_kernel<T><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p);
+    const int threads = row_threads(a.d, 1);
+    const size_t smem = fetch_bytes<T, 2 * kFwdRows>(threads);
+    MOE_CUDA_TRY(cudaFuncSetAttribute(block_norm_vec_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    block_norm_vec_kernel<T><<<p.grid, threads, smem, stream>>>(a, p);
   }
   return last_launch_status();
 }
 
 // Rows at a time and CTAs at once of the backward.
-NormPlan bwd_plan(int T, int d, int group, bool conds) {
-  const int rows = narrow(d) ? kBwdRows : 1;
-  return norm_plan(T, group, conds, rows, 148 * (narrow(d) ? ctas_per_sm(d) : 1));
+template <typename T>
+NormPlan bwd_plan(int tokens, int d, int group, bool conds) {
+  return narrow<T>(d) ? norm_plan(tokens, group, conds, kBwdRows, 148 * ctas_per_sm(d))
+                      : norm_plan(tokens, group, conds, 1, 148);
 }
 
 template <typename T>
 int run_bwd(const BlockNormArgs &a, cudaStream_t stream) {
   const bool conds = a.gate || a.scale || a.dgate || a.dscale || a.dshift;
-  const NormPlan p = bwd_plan(a.T, a.d, a.group, conds);
+  const NormPlan p = bwd_plan<T>(a.T, a.d, a.group, conds);
   const bool cond_out = a.dgate || a.dscale || a.dshift;
   float *part = cond_out && p.per_group > 1 ? a.part : nullptr;
   float *wpart = a.dpre_gamma || a.dpre_beta || a.dpost_gamma
                      ? a.part + (part ? (size_t)p.segments * 3 * a.d : 0) : nullptr;
   if (a.T > 0) {
-    if (!narrow(a.d))
+    if (!narrow<T>(a.d))
       block_norm_bwd_kernel<T><<<p.grid, row_threads(a.d, 2), 0, stream>>>(a, p, part, wpart);
-    else if (a.post == MOE_NORM_NONE)
-      block_norm_bwd_vec_kernel<T, false><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p, part, wpart);
-    else
-      block_norm_bwd_vec_kernel<T, true><<<p.grid, row_threads(a.d, 1), 0, stream>>>(a, p, part, wpart);
+    else {
+      const auto kern = a.post == MOE_NORM_NONE ? block_norm_bwd_vec_kernel<T, false> : block_norm_bwd_vec_kernel<T, true>;
+      const int threads = row_threads(a.d, 1);
+      const size_t smem = fetch_bytes<T, 4 * kBwdRows>(threads);
+      MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      kern<<<p.grid, threads, smem, stream>>>(a, p, part, wpart);
+    }
   }
   const int64_t first = part ? 0 : p.groups, last = p.groups + (wpart ? 1 : 0);
   for (int64_t t = first; t < last; t += 65535) {
@@ -960,10 +1002,11 @@ int run_bwd(const BlockNormArgs &a, cudaStream_t stream) {
 }  // namespace
 
 // Partial sums of either way (with or without conditions) the backward can cut the rows.
-size_t block_norm_workspace_bytes(int T, int d, int group) {
+size_t block_norm_workspace_bytes(int T, int d, int group, int dtype) {
   int64_t most = 0;
   for (int conds = 0; conds < 2; ++conds) {
-    const NormPlan p = bwd_plan(T, d, group, conds != 0);
+    const NormPlan p = dtype == MOE_BF16 ? bwd_plan<__nv_bfloat16>(T, d, group, conds != 0)
+                                         : bwd_plan<float>(T, d, group, conds != 0);
     const int64_t n = (p.per_group > 1 ? p.segments : 0) + p.grid;
     if (n > most) most = n;
   }
