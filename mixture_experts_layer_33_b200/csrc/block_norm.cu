@@ -370,20 +370,17 @@ __device__ __forceinline__ void block_sum_vec(float (&v)[K], VecReducer &red) {
   for (int o = kRest / 2; o > 0; o >>= 1) k[0] += __shfl_xor_sync(0xffffffffu, k[0], o);
   float *b = red.buf + red.turn * kVecWarps * 8;
   red.turn ^= 1;
-  if ((lane & (kRest - 1)) == 0) b[warp * 8 + idx] = k[0];
+  if ((lane & (kRest - 1)) == 0) b[warp * K + idx] = k[0];
   __syncthreads();
+  // Lane l adds up value l mod K over every 32 / K-th warp.
+  float t = 0.f;
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = 0.f;
-  for (int w = 0; w < nw; ++w) {
+  for (int i = 0; i < kVecWarps * K; i += 32)
+    if (i + lane < nw * K) t += b[i + lane];
 #pragma unroll
-    for (int i = 0; i < K; i += 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(b + w * 8 + i);
-      v[i] += f.x;
-      v[i + 1] += f.y;
-      v[i + 2] += f.z;
-      v[i + 3] += f.w;
-    }
-  }
+  for (int o = K; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = __shfl_sync(0xffffffffu, t, i);
 }
 
 // A segment's conditions and weights are folded into three factors per
@@ -422,7 +419,7 @@ __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, No
     for (int i = 0; i < R; ++i) s[i] = dot_v8(v[i], v[i]);
     block_sum_vec(s, red);
 #pragma unroll
-    for (int i = 0; i < R; ++i) r[i] = 1.0f / sqrtf(fmaf(s[i], inv_d, a.eps));
+    for (int i = 0; i < R; ++i) r[i] = rsqrtf(fmaf(s[i], inv_d, a.eps));
   };
   for (int64_t seg = g_lo; seg < g_hi; ++seg) {
     const Segment sg = segment_of(p, seg, a.T);
@@ -612,7 +609,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
         if (!POST) m[i] = rows.get(4 * i + 2);
         if (dz) {
           const V8 q = rows.get(4 * i + 1);
-          const float r = 1.0f / sqrtf(fmaf(s[i], inv_d, a.eps));
+          const float r = rsqrtf(fmaf(s[i], inv_d, a.eps));
           const float k = r * (s[R + i] * inv_d) * r;  // mean(g n), times r: n is r yc
           const uint64_t rr = f2_splat(r), c0 = f2_splat(-r * mg[i]), c1 = f2_splat(-k);
 #pragma unroll
@@ -628,7 +625,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
           for (int j = 0; j < 4; ++j) o.v[j] = f2_mul(alpha, t[i].v[j]);
           store_v8(dx + (size_t)(s0 + i) * a.d + c, o);
         }
-        if (POST) rh[i] = 1.0f / sqrtf(fmaf(s[POST ? 2 * R + i : 0], inv_d, a.eps));
+        if (POST) rh[i] = rsqrtf(fmaf(s[POST ? 2 * R + i : 0], inv_d, a.eps));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (POST) m[i].v[j] = f2_mul(m[i].v[j], f2_splat(rh[i]));
@@ -885,48 +882,57 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(BlockNormArgs a, No
 
 // Sums the partial blocks in order: blockIdx.y < groups adds a group's
 // segments into its condition gradients, the next one the CTAs' sums into
-// the weights' gradients. 32 columns by kSlices slices of the list per CTA.
+// the weights' gradients. 128 columns by kSlices slices of the list per CTA.
 constexpr int kSlices = 16;
 template <typename T>
-__global__ void __launch_bounds__(32 * kSlices) block_norm_sum_kernel(BlockNormArgs a, const float *part, const float *wpart,
-                                                             int64_t first_task, int64_t groups, int per_group,
-                                                             int ctas) {
-  __shared__ float sh[3][kSlices][33];
+__global__ void __launch_bounds__(32 * kSlices) block_norm_sum_kernel(BlockNormArgs a, const float *part,
+                                                                      const float *wpart, int64_t first_task,
+                                                                      int64_t groups, int per_group, int ctas) {
+  __shared__ __align__(16) float sh[3][kSlices][128];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t task = first_task + blockIdx.y;
   const bool cond = part && task < groups;
-  const float *src = cond ? part + (size_t)task * per_group * 3 * a.d : wpart;
-  const int n = cond ? per_group : ctas;
-  const int col = blockIdx.x * 32 + lane;
-  float v[3] = {0.f, 0.f, 0.f};
-  if (col < a.d) {
-    const int lo = (int)((int64_t)n * slice / kSlices), hi = (int)((int64_t)n * (slice + 1) / kSlices);
+  const int n = cond ? per_group : ctas, c0 = blockIdx.x * 128;
+  const float *src = (cond ? part + (size_t)task * per_group * 3 * a.d : wpart) + c0 + lane * 4;
+  float4 v[3];
+#pragma unroll
+  for (int w = 0; w < 3; ++w) v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c0 + lane * 4 < a.d) {
+    const int lo = (int)((unsigned)(n * slice) / kSlices), hi = (int)((unsigned)(n * (slice + 1)) / kSlices);
 #pragma unroll 4
     for (int k = lo; k < hi; ++k)
 #pragma unroll
-      for (int w = 0; w < 3; ++w) v[w] += src[((size_t)k * 3 + w) * a.d + col];
+      for (int w = 0; w < 3; ++w) {
+        const float4 f = *reinterpret_cast<const float4 *>(src + ((size_t)k * 3 + w) * a.d);
+        v[w].x += f.x;
+        v[w].y += f.y;
+        v[w].z += f.z;
+        v[w].w += f.w;
+      }
   }
 #pragma unroll
-  for (int w = 0; w < 3; ++w) sh[w][slice][lane] = v[w];
+  for (int w = 0; w < 3; ++w) *reinterpret_cast<float4 *>(&sh[w][slice][lane * 4]) = v[w];
   __syncthreads();
-  if (slice != 0 || col >= a.d) return;
+  const int col = c0 + threadIdx.x;
+  if (threadIdx.x >= 128 || col >= a.d) return;
+  float t[3];
 #pragma unroll
   for (int w = 0; w < 3; ++w) {
-    v[w] = 0.f;
+    t[w] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kSlices; ++k) v[w] += sh[w][k][lane];
+    for (int k = 0; k < kSlices; ++k) t[w] += sh[w][k][threadIdx.x];
   }
   if (cond) {
     const size_t at = (size_t)task * a.dcond_stride + col;
     const T *pg = static_cast<const T *>(a.pre_gamma), *pb = static_cast<const T *>(a.pre_beta),
             *po = static_cast<const T *>(a.post_gamma);
-    if (a.dshift) a.dshift[at] = v[0];
-    if (a.dscale) a.dscale[at] = fmaf(pg ? to_f32(pg[col]) : 1.f, v[1], pb ? to_f32(pb[col]) * v[0] : 0.f);
-    if (a.dgate) a.dgate[at] = (po ? to_f32(po[col]) : 1.f) * v[2];
+    if (a.dshift) a.dshift[at] = t[0];
+    if (a.dscale) a.dscale[at] = fmaf(pg ? to_f32(pg[col]) : 1.f, t[1], pb ? to_f32(pb[col]) * t[0] : 0.f);
+    if (a.dgate) a.dgate[at] = (po ? to_f32(po[col]) : 1.f) * t[2];
   } else {
-    if (a.dpre_gamma) a.dpre_gamma[col] = v[0];
-    if (a.dpre_beta) a.dpre_beta[col] = v[1];
-    if (a.dpost_gamma) a.dpost_gamma[col] = v[2];
+    if (a.dpre_gamma) a.dpre_gamma[col] = t[0];
+    if (a.dpre_beta) a.dpre_beta[col] = t[1];
+    if (a.dpost_gamma) a.dpost_gamma[col] = t[2];
   }
 }
 
@@ -993,7 +999,7 @@ int run_bwd(const BlockNormArgs &a, cudaStream_t stream) {
   const int64_t first = part ? 0 : p.groups, last = p.groups + (wpart ? 1 : 0);
   for (int64_t t = first; t < last; t += 65535) {
     const unsigned n = (unsigned)(last - t < 65535 ? last - t : 65535);
-    block_norm_sum_kernel<T><<<dim3((a.d + 31) / 32, n), 32 * kSlices, 0, stream>>>(a, part, wpart, t, p.groups,
+    block_norm_sum_kernel<T><<<dim3((a.d + 127) / 128, n), 32 * kSlices, 0, stream>>>(a, part, wpart, t, p.groups,
                                                                                    p.per_group, a.T > 0 ? p.grid : 0);
   }
   return last_launch_status();
