@@ -284,12 +284,11 @@ __device__ __forceinline__ V8 unpack_v8(const float *p) {
   r.v[3] = f2_pack(b.z, b.w);
   return r;
 }
-// This thread's 8 columns of rows on their way: a ring of kFetch steps of N
-// vectors (rows by operands) in shared memory, filled by cp.async two steps
-// ahead. A thread reads only what it copied, so no barrier is involved.
-constexpr int kFetch = 3;
-template <typename T, int N> struct Fetch {
-  T *mine;  // [kFetch][N][blockDim.x][8], this thread's part
+// This thread's 8 columns of rows on their way: a ring of DEPTH steps of N
+// vectors (rows by operands) in shared memory, filled by cp.async DEPTH - 1
+// steps ahead. A thread reads only what it copied, so no barrier is involved.
+template <typename T, int N, int DEPTH> struct Fetch {
+  T *mine;  // [DEPTH][N][blockDim.x][8], this thread's part
   int slot;
   __device__ __forceinline__ T *at(int step, int k) const {
     return mine + (size_t)(step * N + k) * blockDim.x * 8;
@@ -310,11 +309,13 @@ template <typename T, int N> struct Fetch {
   template <int later> __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(later) : "memory");
   }
-  __device__ __forceinline__ void next() { slot = slot == kFetch - 1 ? 0 : slot + 1; }
-  __device__ __forceinline__ int last() const { return slot == 0 ? kFetch - 1 : slot - 1; }
+  __device__ __forceinline__ void next() { slot = slot == DEPTH - 1 ? 0 : slot + 1; }
+  __device__ __forceinline__ int last() const { return slot == 0 ? DEPTH - 1 : slot - 1; }
   __device__ __forceinline__ V8 get(int k) const { return unpack_v8(at(slot, k)); }
 };
-template <typename T, int N> size_t fetch_bytes(int threads) { return (size_t)kFetch * N * threads * 8 * sizeof(T); }
+template <typename T, int N, int DEPTH> size_t fetch_bytes(int threads) {
+  return (size_t)DEPTH * N * threads * 8 * sizeof(T);
+}
 template <typename T>
 __device__ __forceinline__ void store_v8(T *p, const V8 &a) {
   float f[8];
@@ -386,14 +387,19 @@ __device__ __forceinline__ void block_sum_vec(float (&v)[K], VecReducer &red) {
 // A segment's conditions and weights are folded into three factors per
 // column, fg = gate post_gamma, fs = (1 + scale) pre_gamma, fb = (1 + scale)
 // pre_beta + shift: y = res_scale x + fg N(h), z = fs N(y) + fb.
-constexpr int kFwdRows = 4;
-template <typename T>
-__global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, NormPlan p) {
+constexpr int kFwdRows = 4, kFwdDepth = 2;
+// CTAs per SM of the kernels for many rows, with at most MAXT threads (at
+// 1152 columns the forward gains from a fourth, 16.8 -> 15.9 us; the backward
+// would spill for it).
+constexpr int fwd_ctas(int maxt) { return maxt <= 160 ? 4 : maxt <= 256 ? 2 : 1; }
+constexpr int bwd_ctas(int maxt) { return maxt <= 160 ? 3 : maxt <= 256 ? 2 : 1; }
+template <typename T, int MAXT>
+__global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) block_norm_vec_kernel(BlockNormArgs a, NormPlan p) {
   constexpr int R = kFwdRows;
   __shared__ __align__(16) float red_buf[2 * kVecWarps * 8];
   extern __shared__ __align__(16) uint8_t ring[];
   VecReducer red{red_buf, 0};
-  Fetch<T, 2 * R> rows{reinterpret_cast<T *>(ring) + threadIdx.x * 8, 0};
+  Fetch<T, 2 * R, kFwdDepth> rows{reinterpret_cast<T *>(ring) + threadIdx.x * 8, 0};
   const T *h = static_cast<const T *>(a.h), *x = static_cast<const T *>(a.x);  // either may be y
   T *y = static_cast<T *>(a.y), *z = static_cast<T *>(a.z);
   const int c = threadIdx.x * 8;
@@ -436,8 +442,8 @@ __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, No
     };
     rows.template wait<0>();  // the last segment's copies past its end
     rows.slot = 0;
-    fetch(sg.lo, 0);
-    fetch(sg.lo + R, 1);
+#pragma unroll
+    for (int k = 0; k < kFwdDepth - 1; ++k) fetch(sg.lo + k * R, k);
     const size_t cond = (size_t)sg.group * a.cond_stride + c;
     V8 fg = load_v8_or(static_cast<const T *>(a.gate), cond, col, 1.f);
     V8 fs = load_v8_or(static_cast<const T *>(a.scale), cond, col, 0.f);
@@ -455,8 +461,8 @@ __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, No
       }
     }
     for (int s0 = sg.lo; s0 < sg.hi; s0 += R) {
-      fetch(s0 + 2 * R, rows.last());
-      rows.template wait<2>();
+      fetch(s0 + (kFwdDepth - 1) * R, rows.last());
+      rows.template wait<kFwdDepth - 1>();
       V8 u[R];
       float r[R];
 #pragma unroll
@@ -497,15 +503,15 @@ __global__ void __launch_bounds__(512) block_norm_vec_kernel(BlockNormArgs a, No
 // so that mean(y) and mean(g), then mean(yc^2) and mean(g yc), and the same
 // of h, each take one reduction. Sums of a segment as in the other kernels;
 // the CTA's sums for the weights are kept in wpart, which only it touches.
-constexpr int kBwdRows = 2;
-template <typename T, bool POST>
-__global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a, NormPlan p, float *part,
+constexpr int kBwdRows = 2, kBwdDepth = 3;
+template <typename T, bool POST, int MAXT>
+__global__ void __launch_bounds__(MAXT, bwd_ctas(MAXT)) block_norm_bwd_vec_kernel(BlockNormArgs a, NormPlan p, float *part,
                                                                  float *wpart) {
   constexpr int R = kBwdRows;
   __shared__ __align__(16) float red_buf[2 * kVecWarps * 8];
   extern __shared__ __align__(16) uint8_t ring[];
   VecReducer red{red_buf, 0};
-  Fetch<T, 4 * R> rows{reinterpret_cast<T *>(ring) + threadIdx.x * 8, 0};
+  Fetch<T, 4 * R, kBwdDepth> rows{reinterpret_cast<T *>(ring) + threadIdx.x * 8, 0};
   const T *h = static_cast<const T *>(a.h), *y = static_cast<const T *>(a.yin);
   const T *dz = static_cast<const T *>(a.dz), *dy = static_cast<const T *>(a.dy);  // either may be dh or dx
   T *dh = static_cast<T *>(a.dh), *dx = static_cast<T *>(a.dx);
@@ -535,8 +541,8 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
     };
     rows.template wait<0>();  // the last segment's copies past its end
     rows.slot = 0;
-    fetch(sg.lo, 0);
-    fetch(sg.lo + R, 1);
+#pragma unroll
+    for (int k = 0; k < kBwdDepth - 1; ++k) fetch(sg.lo + k * R, k);
     const size_t cond = (size_t)sg.group * a.cond_stride + c;
     V8 fz = load_v8_or(static_cast<const T *>(a.scale), cond, col, 0.f);
     V8 fh = load_v8_or(static_cast<const T *>(a.gate), cond, col, 1.f);
@@ -555,8 +561,8 @@ __global__ void __launch_bounds__(512) block_norm_bwd_vec_kernel(BlockNormArgs a
       }
     }
     for (int s0 = sg.lo; s0 < sg.hi; s0 += R) {
-      fetch(s0 + 2 * R, rows.last());
-      rows.template wait<2>();
+      fetch(s0 + (kBwdDepth - 1) * R, rows.last());
+      rows.template wait<kBwdDepth - 1>();
       V8 t[R], m[R], n[R], g[R];
       float rh[R];
 #pragma unroll
@@ -880,25 +886,39 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(BlockNormArgs a, No
     }
 }
 
-// Sums the partial blocks in order: blockIdx.y < groups adds a group's
-// segments into its condition gradients, the next one the CTAs' sums into
-// the weights' gradients. 128 columns by kSlices slices of the list per CTA.
-constexpr int kSlices = 16;
+// Sums lists of partial blocks [n][3][d] in order, 128 columns by kSlices
+// slices of a list per CTA. List blockIdx.y < groups is a group's segments and
+// gives its condition gradients; the ones after are kWeightLists parts of the
+// CTAs' sums for the weights (hundreds of entries: one CTA per 128 columns
+// would take them in at one SM's bandwidth), whose sums go to wsum; a launch
+// over wsum (`last`) gives the weights' gradients.
+constexpr int kSlices = 16, kWeightLists = 16;
+struct NormSums {
+  const float *part, *wpart;
+  float *wsum;
+  int64_t first, groups;  // first: the list of blockIdx.y = 0
+  int per_group, ctas, last;
+};
 template <typename T>
-__global__ void __launch_bounds__(32 * kSlices) block_norm_sum_kernel(BlockNormArgs a, const float *part,
-                                                                      const float *wpart, int64_t first_task,
-                                                                      int64_t groups, int per_group, int ctas) {
+__global__ void __launch_bounds__(32 * kSlices) block_norm_sum_kernel(BlockNormArgs a, NormSums q) {
   __shared__ __align__(16) float sh[3][kSlices][128];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t task = first_task + blockIdx.y;
-  const bool cond = part && task < groups;
-  const int n = cond ? per_group : ctas, c0 = blockIdx.x * 128;
-  const float *src = (cond ? part + (size_t)task * per_group * 3 * a.d : wpart) + c0 + lane * 4;
+  const int64_t list = q.first + blockIdx.y;
+  const bool cond = list < q.groups;
+  const int part = (int)(list - q.groups), c0 = blockIdx.x * 128;
+  int n = q.per_group;
+  const float *src = q.part + (size_t)list * q.per_group * 3 * a.d;
+  if (!cond) {
+    const int lo = q.last ? 0 : q.ctas * part / kWeightLists;
+    n = q.last ? kWeightLists : q.ctas * (part + 1) / kWeightLists - lo;
+    src = (q.last ? q.wsum : q.wpart) + (size_t)lo * 3 * a.d;
+  }
+  src += c0 + lane * 4;
   float4 v[3];
 #pragma unroll
   for (int w = 0; w < 3; ++w) v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c0 + lane * 4 < a.d) {
-    const int lo = (int)((unsigned)(n * slice) / kSlices), hi = (int)((unsigned)(n * (slice + 1)) / kSlices);
+    const int lo = n * slice / kSlices, hi = n * (slice + 1) / kSlices;
 #pragma unroll 4
     for (int k = lo; k < hi; ++k)
 #pragma unroll
@@ -923,12 +943,15 @@ __global__ void __launch_bounds__(32 * kSlices) block_norm_sum_kernel(BlockNormA
     for (int k = 0; k < kSlices; ++k) t[w] += sh[w][k][threadIdx.x];
   }
   if (cond) {
-    const size_t at = (size_t)task * a.dcond_stride + col;
+    const size_t at = (size_t)list * a.dcond_stride + col;
     const T *pg = static_cast<const T *>(a.pre_gamma), *pb = static_cast<const T *>(a.pre_beta),
             *po = static_cast<const T *>(a.post_gamma);
     if (a.dshift) a.dshift[at] = t[0];
     if (a.dscale) a.dscale[at] = fmaf(pg ? to_f32(pg[col]) : 1.f, t[1], pb ? to_f32(pb[col]) * t[0] : 0.f);
     if (a.dgate) a.dgate[at] = (po ? to_f32(po[col]) : 1.f) * t[2];
+  } else if (!q.last) {
+#pragma unroll
+    for (int w = 0; w < 3; ++w) q.wsum[((size_t)part * 3 + w) * a.d + col] = t[w];
   } else {
     if (a.dpre_gamma) a.dpre_gamma[col] = t[0];
     if (a.dpre_beta) a.dpre_beta[col] = t[1];
@@ -946,10 +969,10 @@ int row_threads(int d, int nv) {
 // time (the backward spills there: 12 arrays of 16 columns do not fit 128
 // registers).
 template <typename T> inline bool narrow(int d) { return d * (int)sizeof(T) <= 8192; }
-// CTAs per SM of the kernels for many rows (128 registers a thread).
-inline int ctas_per_sm(int d) {
-  const int n = 512 / row_threads(d, 1);
-  return n > 8 ? 8 : n;
+// The kernels for many rows are built for three bounds on the threads.
+inline int thread_bound(int d) {
+  const int t = row_threads(d, 1);
+  return t <= 160 ? 160 : t <= 256 ? 256 : 512;
 }
 
 template <typename T>
@@ -961,11 +984,15 @@ int run_fwd(const BlockNormArgs &a, cudaStream_t stream) {
   } else if (a.T <= 2 * sms) {  // few tokens: a CTA each
     block_norm_kernel<T, 1, 1><<<a.T, row_threads(a.d, 1), 0, stream>>>(a);
   } else {
-    const NormPlan p = norm_plan(a.T, a.group, a.gate || a.scale || a.shift, kFwdRows, (int)sms * ctas_per_sm(a.d));
-    const int threads = row_threads(a.d, 1);
-    const size_t smem = fetch_bytes<T, 2 * kFwdRows>(threads);
-    MOE_CUDA_TRY(cudaFuncSetAttribute(block_norm_vec_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    block_norm_vec_kernel<T><<<p.grid, threads, smem, stream>>>(a, p);
+    const NormPlan p = norm_plan(a.T, a.group, a.gate || a.scale || a.shift, kFwdRows,
+                                 (int)sms * fwd_ctas(thread_bound(a.d)));
+    const int threads = row_threads(a.d, 1), bound = thread_bound(a.d);
+    const auto kern = bound == 160   ? block_norm_vec_kernel<T, 160>
+                      : bound == 256 ? block_norm_vec_kernel<T, 256>
+                                     : block_norm_vec_kernel<T, 512>;
+    const size_t smem = fetch_bytes<T, 2 * kFwdRows, kFwdDepth>(threads);
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    kern<<<p.grid, threads, smem, stream>>>(a, p);
   }
   return last_launch_status();
 }
@@ -973,8 +1000,15 @@ int run_fwd(const BlockNormArgs &a, cudaStream_t stream) {
 // Rows at a time and CTAs at once of the backward.
 template <typename T>
 NormPlan bwd_plan(int tokens, int d, int group, bool conds) {
-  return narrow<T>(d) ? norm_plan(tokens, group, conds, kBwdRows, 148 * ctas_per_sm(d))
+  return narrow<T>(d) ? norm_plan(tokens, group, conds, kBwdRows, 148 * bwd_ctas(thread_bound(d)))
                       : norm_plan(tokens, group, conds, 1, 148);
+}
+
+template <typename T, bool POST>
+auto bwd_kernel(int bound) {
+  return bound == 160   ? block_norm_bwd_vec_kernel<T, POST, 160>
+         : bound == 256 ? block_norm_bwd_vec_kernel<T, POST, 256>
+                        : block_norm_bwd_vec_kernel<T, POST, 512>;
 }
 
 template <typename T>
@@ -989,18 +1023,26 @@ int run_bwd(const BlockNormArgs &a, cudaStream_t stream) {
     if (!narrow<T>(a.d))
       block_norm_bwd_kernel<T><<<p.grid, row_threads(a.d, 2), 0, stream>>>(a, p, part, wpart);
     else {
-      const auto kern = a.post == MOE_NORM_NONE ? block_norm_bwd_vec_kernel<T, false> : block_norm_bwd_vec_kernel<T, true>;
-      const int threads = row_threads(a.d, 1);
-      const size_t smem = fetch_bytes<T, 4 * kBwdRows>(threads);
+      const int threads = row_threads(a.d, 1), bound = thread_bound(a.d);
+      const auto kern = a.post == MOE_NORM_NONE ? bwd_kernel<T, false>(bound) : bwd_kernel<T, true>(bound);
+      const size_t smem = fetch_bytes<T, 4 * kBwdRows, kBwdDepth>(threads);
       MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
       kern<<<p.grid, threads, smem, stream>>>(a, p, part, wpart);
     }
   }
-  const int64_t first = part ? 0 : p.groups, last = p.groups + (wpart ? 1 : 0);
-  for (int64_t t = first; t < last; t += 65535) {
-    const unsigned n = (unsigned)(last - t < 65535 ? last - t : 65535);
-    block_norm_sum_kernel<T><<<dim3((a.d + 127) / 128, n), 32 * kSlices, 0, stream>>>(a, part, wpart, t, p.groups,
-                                                                                   p.per_group, a.T > 0 ? p.grid : 0);
+  NormSums q{};
+  q.part = part; q.wpart = wpart; q.wsum = wpart + (size_t)p.grid * 3 * a.d;
+  q.groups = p.groups; q.per_group = p.per_group; q.ctas = a.T > 0 ? p.grid : 0;
+  const unsigned blocks = (a.d + 127) / 128;
+  const int64_t end = p.groups + (wpart ? kWeightLists : 0);
+  for (q.first = part ? 0 : p.groups; q.first < end; q.first += 65535) {
+    const unsigned n = (unsigned)(end - q.first < 65535 ? end - q.first : 65535);
+    block_norm_sum_kernel<T><<<dim3(blocks, n), 32 * kSlices, 0, stream>>>(a, q);
+  }
+  if (wpart) {
+    q.first = p.groups;
+    q.last = 1;
+    block_norm_sum_kernel<T><<<dim3(blocks, 1), 32 * kSlices, 0, stream>>>(a, q);
   }
   return last_launch_status();
 }
@@ -1013,7 +1055,7 @@ size_t block_norm_workspace_bytes(int T, int d, int group, int dtype) {
   for (int conds = 0; conds < 2; ++conds) {
     const NormPlan p = dtype == MOE_BF16 ? bwd_plan<__nv_bfloat16>(T, d, group, conds != 0)
                                          : bwd_plan<float>(T, d, group, conds != 0);
-    const int64_t n = (p.per_group > 1 ? p.segments : 0) + p.grid;
+    const int64_t n = (p.per_group > 1 ? p.segments : 0) + p.grid + kWeightLists;
     if (n > most) most = n;
   }
   return (size_t)most * 3 * d * 4;
