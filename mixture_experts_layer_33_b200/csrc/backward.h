@@ -31,12 +31,12 @@ struct ExchangeBwdArgs {
   const void *y_perm;
   void *dy_perm;
   float *dw, *dconst;
-  float *const_part;  // workspace of const_grad_workspace_bytes()
+  float *const_part;  // workspace of const_grad_workspace_bytes(): chunk sums, then
+  float2 *const_coef; // (set by the launcher) w a1 and q of each assignment
   // dispatch
   const void *dx_perm;
   const void *add[3];
   void *dx;
-  int fine;  // set by the launcher: one 256-feature chunk per warp item
   int32_t *dev_status;
 };
 size_t const_grad_workspace_bytes(int64_t n_assign, int n_const, int d, int const_mix);
