@@ -505,8 +505,8 @@ MOE_API int moe_combine_backward(const moe_config *cfg, const void *dy, const vo
  * added in the same pass:
  *   dx_s = add0_s + add1_s + add2_s + sum_a { dx_perm[row_of[a]]  (heavy),
  *          w_a dy_s (identity), a0 g + q (Wc_0 - Wc_1) (mixed constant) }
- * summed in fp32 (the added gradients, dy_s with all its coefficients, then
- * the rows in slot order) and rounded once; g and q as above.
+ * summed in fp32 (the rows in slot order, dy_s with all its coefficients, then
+ * the added gradients) and rounded once; g and q as above.
  *   dx_perm  [n_assign, d] (dtype), nullable when n_heavy == 0
  *   dy, x    [T, d]; dy is needed with identity or mixed constant experts,
  *            x and const_vecs with mixed constant experts, else nullable

@@ -21,37 +21,55 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// 8 values as loaded (zeros unless `live`), kept apart from their conversion
-// so that every load of a pass is issued before the first is waited for.
+// Volatile: the loads of a pass are issued here, all before the first is
+// waited for (the compiler would move a load down to its use, which made one
+// round trip to HBM into three in the dispatch).
+__device__ __forceinline__ uint4 load16(const void *p) {
+  uint4 u;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
+// Zeros unless `live`, without a branch.
+__device__ __forceinline__ uint4 load16(const void *p, bool live) {
+  uint4 u;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(u.x), "=&r"(u.y), "=&r"(u.z), "=&r"(u.w)
+      : "l"(p), "r"((int)live));
+  return u;
+}
+// 8 values as loaded, kept apart from their conversion.
 template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> {
   uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool live) {
-    u = make_uint4(0, 0, 0, 0);
-    if (live) u = *reinterpret_cast<const uint4 *>(p);
-  }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = load16(p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool live) { u = load16(p, live); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __bfloat1622float2(h[i]);
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
+    for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its fp32
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
 };
 template <> struct Raw8<float> {
-  float4 a, b;
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = load16(p);
+    b = load16(p + 4);
+  }
   __device__ __forceinline__ void load(const float *p, bool live) {
-    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-      a = *reinterpret_cast<const float4 *>(p);
-      b = *reinterpret_cast<const float4 *>(p + 4);
-    }
+    a = load16(p, live);
+    b = load16(p + 4, live);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
   }
 };
 
@@ -115,7 +133,7 @@ __device__ __forceinline__ bool assignment_of(const ExchangeBwdArgs &a, int64_t 
 // are in flight together. 16384 rows of 1152 (94 MB): 18 us, with a 14.4 us
 // floor.
 constexpr int kRowPass = 5;
-template <typename T>
+template <typename T, bool MIX>
 __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(ExchangeBwdArgs a, KindTable kinds) {
   const T *__restrict__ dy = static_cast<const T *>(a.dy);
   const T *__restrict__ yp = static_cast<const T *>(a.y_perm);
@@ -142,13 +160,13 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(ExchangeBwdArgs a
       } else if (kind == MOE_IDENTITY) {
         src = x + (size_t)s * a.d;
       } else if (kind == MOE_CONST) {
-        src = cv + (size_t)kinds.cidx[e] * (a.const_mix ? 3 : 1) * a.d;
-        mix = a.const_mix != 0;
+        src = cv + (size_t)kinds.cidx[e] * (MIX ? 3 : 1) * a.d;
+        mix = MIX;
       }
     }
     const T *g = dy + (size_t)s * a.d;
     float dot = 0.f;
-    if (mix) {
+    if (MIX && mix) {
       const MixDots m = mix_dots(x + (size_t)s * a.d, g, src, a.d);
       dot = m.a0 * m.gx + m.a1 * m.gv;
       if (a.dconst && lane == 0) {
@@ -292,173 +310,179 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices / 4) const_grad_sum_kern
 
 // ---- dispatch
 //
-// A CTA takes a few tokens. First a warp per token walks its slots (token
-// list -> row: a chain of dependent loads) and leaves each slot's source in
-// shared memory: the row of the expert's input gradient, or for a mixed
-// constant expert (MIX; the others' kernel leaves that out) its Wc rows and
-// coefficient q, and the sum of the coefficients of dy_s itself. Then the
-// warps take the tokens' 256-feature chunks, all of whose sources are known
-// and in flight together. 8192 tokens of 2048, expert choice (168 MB): 33 us
-// of a 26 us floor; with a warp per token and chunk pair, each walking the
-// chain, 48 us.
-constexpr int kMaxTok = 8;        // tokens per CTA
-constexpr int kMaxSlots = 128;    // slots of a token kept in shared memory (the rest are read where they are used)
-constexpr int kBatch = 4;         // slots whose rows are in flight together
-
-struct Slot {
+// One warp per PASS 256-feature chunks of a token. The token's slots are read
+// once, one per lane, and turned into a source: the row of the expert's input
+// gradient, or for a mixed constant expert (MIX; the others' kernel leaves
+// that out) its Wc rows with coefficient q, and the coefficient of dy_s. The
+// chain token list -> assignment -> row -> values is four round trips; warps
+// enough to hide it stay resident only with few registers, so two chunks and
+// BATCH slots at a time. 8192 tokens of 2048 under expert choice with two
+// added gradients (168 MB): 38 us, where a copy of as many bytes takes 35. A
+// warp that walks the lists ahead of the others took 45 us, four chunks a warp
+// or four tokens in a row 43, one chunk and more warps 42.
+template <bool MIX> struct Slot {
   int row;    // of dx_perm; -1: no source; -2 - c: mixed constant expert c
-  float coef; // q of a mixed constant expert
+  float own;  // coefficient of dy_s: w of an identity, w a0 of a mixed constant expert
+  float coef; // q of a mixed constant expert (before its dots: w)
 };
-// Slot j of the list, without a mixed constant expert's dots; own_g: its
-// coefficient of dy_s.
 template <bool MIX>
-__device__ __forceinline__ Slot slot_of(const ExchangeBwdArgs &a, const KindTable &kinds, bool ec, int j, float &own_g) {
-  Slot r{-1, 0.f};
+__device__ __forceinline__ Slot<MIX> slot_of(const ExchangeBwdArgs &a, const KindTable &kinds, bool ec, int j) {
+  Slot<MIX> r{-1, 0.f, 0.f};
   const int asg = ec ? a.tok_assign[j] : j;
   if (asg < 0 || asg >= a.n_assign) {
     set_status(a.dev_status, MOE_DEV_BAD_INDEX);
     return r;
   }
-  const int e = ec ? (int)(((unsigned)asg / (unsigned)a.C) % (unsigned)a.E) : a.sel[asg];
   const int row = a.row_of[asg];
+  const int e = ec ? (int)(((unsigned)asg / (unsigned)a.C) % (unsigned)a.E) : a.sel[asg];
   if (e < 0 || e >= a.E) return r;
   const int kind = kinds.kind[e];
   if (kind == MOE_HEAVY) {
     if (row < a.n_assign) r.row = row < 0 ? -1 : row;
     else set_status(a.dev_status, MOE_DEV_BAD_INDEX);
   } else if (kind == MOE_IDENTITY) {
-    own_g += a.w[asg];
+    r.own = a.w[asg];
   } else if (MIX && kind == MOE_CONST) {
     r.row = -2 - kinds.cidx[e];
     r.coef = a.w[asg];
   }
   return r;
 }
-// The whole warp: a mixed constant expert's w becomes q; w a0 is returned.
-template <typename T>
-__device__ __forceinline__ float mix_slot(const ExchangeBwdArgs &a, int s, Slot &r) {
-  const size_t at = (size_t)s * a.d;
-  const MixDots m = mix_dots(static_cast<const T *>(a.x) + at, static_cast<const T *>(a.dy) + at,
-                             static_cast<const T *>(a.const_vecs) + (size_t)(-2 - r.row) * 3 * a.d, a.d);
-  const float w = r.coef;
-  r.coef = m.a0 * m.a1 * (w * m.gx - w * m.gv);
-  return w * m.a0;
+
+// 8 fp32 sums as packed pairs.
+struct Acc8 {
+  uint64_t v[4];
+  __device__ __forceinline__ void add(const float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v[i]) : "l"(f2_pack(f[2 * i], f[2 * i + 1])));
+  }
+  __device__ __forceinline__ void fma(float w, const float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_fma(f2_splat(w), f2_pack(f[2 * i], f[2 * i + 1]), v[i]);
+  }
+};
+
+template <typename T, bool MIX, int PASS, int BATCH, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) dispatch_bwd_kernel(ExchangeBwdArgs a, KindTable kinds) {
+  const T *dy = static_cast<const T *>(a.dy), *cv = static_cast<const T *>(a.const_vecs);
+  T *dx = static_cast<T *>(a.dx);  // may be any of a.add
+  const int lane = threadIdx.x & 31;
+  const bool ec = a.routing == MOE_EXPERT_CHOICE;
+  const unsigned per_tok = (unsigned)(a.d + 256 * PASS - 1) / (256 * PASS);
+  const unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int s = (int)(item / per_tok), c = (int)(item % per_tok) * 256 * PASS + lane * 8;
+  if (s >= a.T) return;
+  int j_lo = s * a.k, j_hi = j_lo + a.k;
+  if (ec) {
+    j_lo = a.tok_ptr[s];
+    j_hi = a.tok_ptr[s + 1];
+    if (j_lo < 0 || j_hi < j_lo || j_hi > a.n_assign) {  // a token list out of range: no slots
+      if (lane == 0) set_status(a.dev_status, MOE_DEV_BAD_INDEX);
+      j_lo = j_hi = 0;
+    }
+  }
+  // This lane's columns of each chunk; past the row's end it reads others and
+  // stores nothing.
+  int off[PASS];
+#pragma unroll
+  for (int q = 0; q < PASS; ++q) off[q] = c + 256 * q < a.d ? c + 256 * q : 0;
+  const size_t row0 = (size_t)s * a.d;
+  Raw8<T> base[3][PASS];
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (a.add[k]) {
+#pragma unroll
+      for (int q = 0; q < PASS; ++q) base[k][q].load(static_cast<const T *>(a.add[k]) + row0 + off[q]);
+    }
+  Acc8 sum[PASS];
+#pragma unroll
+  for (int q = 0; q < PASS; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[q].v[i] = 0;
+  float own = 0.f, f[8];
+  for (int j0 = j_lo; j0 < j_hi; j0 += 32) {
+    Slot<MIX> mine{-1, 0.f, 0.f};
+    if (j0 + lane < j_hi) mine = slot_of<MIX>(a, kinds, ec, j0 + lane);
+    if (MIX) {
+      for (unsigned mm = __ballot_sync(0xffffffffu, mine.row <= -2); mm; mm &= mm - 1u) {
+        const int q = __ffs(mm) - 1, row = __shfl_sync(0xffffffffu, mine.row, q);
+        const MixDots m =
+            mix_dots(static_cast<const T *>(a.x) + row0, dy + row0, cv + (size_t)(-2 - row) * 3 * a.d, a.d);
+        if (lane == q) {
+          const float w = mine.coef;
+          mine.coef = m.a0 * m.a1 * (w * m.gx - w * m.gv);
+          mine.own = w * m.a0;
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, mine.own != 0.f)) own += warp_sum(mine.own);
+    // Only slots with a source from here on, in order.
+    unsigned left = __ballot_sync(0xffffffffu, mine.row != -1);
+    while (left) {
+      Raw8<T> raw[BATCH][PASS];
+      int row[BATCH];
+      float coef[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        row[u] = -1;
+        if (left == 0) continue;
+        const int q = __ffs(left) - 1;
+        left &= left - 1u;
+        row[u] = __shfl_sync(0xffffffffu, mine.row, q);
+        if (MIX) coef[u] = __shfl_sync(0xffffffffu, mine.coef, q);
+        const T *src = MIX && row[u] < 0 ? cv + ((size_t)(-2 - row[u]) * 3 + 1) * a.d
+                                         : static_cast<const T *>(a.dx_perm) + (size_t)row[u] * a.d;
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) raw[u][i].load(src + off[i]);
+      }
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        if (row[u] == -1) continue;
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) {
+          raw[u][i].get(f);
+          if (MIX && row[u] < 0) {
+            sum[i].fma(coef[u], f);
+            load8(cv + ((size_t)(-2 - row[u]) * 3 + 2) * a.d + off[i], f);
+            sum[i].fma(-coef[u], f);
+          } else {
+            sum[i].add(f);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < PASS; ++q) {
+    if (c + 256 * q >= a.d) continue;
+    if (own != 0.f) {
+      load8(dy + row0 + off[q], f);
+      sum[q].fma(own, f);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (a.add[k]) {
+        base[k][q].get(f);
+        sum[q].add(f);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(sum[q].v[i], f[2 * i], f[2 * i + 1]);
+    store8(dx + row0 + off[q], f);
+  }
 }
 
 template <typename T, bool MIX>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) dispatch_bwd_kernel(ExchangeBwdArgs a,
-                                                                                        KindTable kinds, int tokens) {
-  __shared__ Slot slots[kMaxTok][kMaxSlots];
-  __shared__ int s_first[kMaxTok], s_count[kMaxTok];
-  __shared__ float s_g[kMaxTok];
-  const T *dy = static_cast<const T *>(a.dy), *rows = static_cast<const T *>(a.dx_perm);
-  T *dx = static_cast<T *>(a.dx);  // may be any of a.add
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool ec = a.routing == MOE_EXPERT_CHOICE;
-  const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
-  if (warp < nt) {
-    const int s = t0 + warp;
-    int a0 = s * a.k, n = a.k;
-    if (ec) {
-      a0 = a.tok_ptr[s];
-      n = a.tok_ptr[s + 1] - a0;
-      if (a0 < 0 || n < 0 || a0 + (int64_t)n > a.n_assign) {  // a token list out of range: no slots
-        if (lane == 0) set_status(a.dev_status, MOE_DEV_BAD_INDEX);
-        a0 = n = 0;
-      }
-    }
-    float g = 0.f;
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      Slot r{-1, 0.f};
-      float own = 0.f;
-      if (j0 + lane < n) r = slot_of<MIX>(a, kinds, ec, a0 + j0 + lane, own);
-      if (MIX) {
-        for (unsigned mm = __ballot_sync(0xffffffffu, r.row <= -2); mm; mm &= mm - 1u) {
-          const int q = __ffs(mm) - 1;
-          Slot m{__shfl_sync(0xffffffffu, r.row, q), __shfl_sync(0xffffffffu, r.coef, q)};
-          const float own_q = mix_slot<T>(a, s, m);
-          if (lane == q) {
-            r = m;
-            own += own_q;
-          }
-        }
-      }
-      if (j0 + lane < n && j0 + lane < kMaxSlots) slots[warp][j0 + lane] = r;
-      g += warp_sum(own);
-    }
-    if (lane == 0) {
-      s_first[warp] = a0;
-      s_count[warp] = n;
-      s_g[warp] = g;
-    }
-  }
-  __syncthreads();
-  const int chunks = (a.d + 255) / 256;
-  for (int item = warp; item < nt * chunks; item += kWarps) {
-    const int t = item / chunks, c = (item - t * chunks) * 256 + lane * 8, n = s_count[t];
-    const bool live = c < a.d;
-    const size_t at = (size_t)(t0 + t) * a.d + c;
-    Raw8<T> base[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) base[k].load(static_cast<const T *>(a.add[k]) + at, live && a.add[k]);
-    float acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < n; j0 += kBatch) {
-      Slot r[kBatch];
-      Raw8<T> raw[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        r[u] = Slot{-1, 0.f};
-        if (j0 + u < n) {
-          if (j0 + u < kMaxSlots) {
-            r[u] = slots[t][j0 + u];
-          } else {
-            float unused = 0.f;
-            r[u] = slot_of<MIX>(a, kinds, ec, s_first[t] + j0 + u, unused);
-            if (MIX && r[u].row <= -2) mix_slot<T>(a, t0 + t, r[u]);
-          }
-        }
-        const T *src = rows + (size_t)(r[u].row < 0 ? 0 : r[u].row) * a.d;
-        if (MIX && r[u].row <= -2)
-          src = static_cast<const T *>(a.const_vecs) + ((size_t)(-2 - r[u].row) * 3 + 1) * a.d;
-        raw[u].load(src + c, live && r[u].row != -1);
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        float f[8];
-        raw[u].get(f);
-        if (MIX && r[u].row <= -2) {
-          float f1[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f1[i] = 0.f;
-          if (live) load8(static_cast<const T *>(a.const_vecs) + ((size_t)(-2 - r[u].row) * 3 + 2) * a.d + c, f1);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = fmaf(r[u].coef, f[i] - f1[i], acc[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] += f[i];
-        }
-      }
-    }
-    if (!live) continue;
-    float f[8], o[8];
-    base[0].get(o);
-#pragma unroll
-    for (int k = 1; k < 3; ++k) {
-      base[k].get(f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] += f[i];
-    }
-    if (s_g[t] != 0.f) {
-      load8(dy + at, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(s_g[t], f[i], o[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] += acc[i];
-    store8(dx + at, o);
-  }
+int run_dispatch_bwd(const ExchangeBwdArgs &a, const KindTable &kinds, cudaStream_t stream) {
+  // Two chunks a warp, unless one still leaves SMs idle.
+  const bool few = (int64_t)a.T * ((a.d + 511) / 512) < 16 * (int64_t)num_sms();
+  const int64_t items = (int64_t)a.T * (few ? (a.d + 255) / 256 : (a.d + 511) / 512);
+  const int64_t blocks = (items + kWarps - 1) / kWarps;
+  if (blocks * kWarps > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  constexpr int ctas = sizeof(T) == 2 && !MIX ? 4 : 2;
+  if (few) dispatch_bwd_kernel<T, MIX, 1, 8, 2><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kinds);
+  else dispatch_bwd_kernel<T, MIX, 2, 2, ctas><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kinds);
+  return last_launch_status();
 }
 
 }  // namespace
@@ -477,8 +501,10 @@ int launch_combine_bwd(const ExchangeBwdArgs &args, const KindTable &kinds, cuda
   a.const_coef = reinterpret_cast<float2 *>(a.const_part + (size_t)chunks * n);
   if (a.n_assign > 0) {
     const int64_t blocks = (a.n_assign + kWarps - 1) / kWarps;  // below 2^28: assignments fit 31 bits
-    if (bf16) combine_bwd_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kinds);
-    else combine_bwd_kernel<float><<<(unsigned)blocks, kThreads, 0, stream>>>(a, kinds);
+    const bool mix = a.n_const > 0 && a.const_mix;
+    const auto b = mix ? combine_bwd_kernel<__nv_bfloat16, true> : combine_bwd_kernel<__nv_bfloat16, false>;
+    const auto f = mix ? combine_bwd_kernel<float, true> : combine_bwd_kernel<float, false>;
+    (bf16 ? b : f)<<<(unsigned)blocks, kThreads, 0, stream>>>(a, kinds);
   }
   if (a.dconst && a.n_const > 0) {
     const dim3 grid(chunks, a.n_const, (a.d + kThreads * 8 - 1) / (kThreads * 8));
@@ -493,15 +519,11 @@ int launch_combine_bwd(const ExchangeBwdArgs &args, const KindTable &kinds, cuda
 
 int launch_dispatch_bwd(const ExchangeBwdArgs &a, const KindTable &kinds, cudaStream_t stream) {
   if (a.T == 0) return MOE_OK;
-  // As many tokens per CTA as still leave four CTAs for each SM.
-  int tokens = a.T / (4 * num_sms());
-  tokens = tokens < 1 ? 1 : tokens > kMaxTok ? kMaxTok : tokens;
-  const unsigned blocks = (unsigned)((a.T + tokens - 1) / tokens);
   const bool mix = a.n_const > 0 && a.const_mix;
-  const auto b = mix ? dispatch_bwd_kernel<__nv_bfloat16, true> : dispatch_bwd_kernel<__nv_bfloat16, false>;
-  const auto f = mix ? dispatch_bwd_kernel<float, true> : dispatch_bwd_kernel<float, false>;
-  (a.dtype == MOE_BF16 ? b : f)<<<blocks, kThreads, 0, stream>>>(a, kinds, tokens);
-  return last_launch_status();
+  if (a.dtype == MOE_BF16)
+    return mix ? run_dispatch_bwd<__nv_bfloat16, true>(a, kinds, stream)
+               : run_dispatch_bwd<__nv_bfloat16, false>(a, kinds, stream);
+  return mix ? run_dispatch_bwd<float, true>(a, kinds, stream) : run_dispatch_bwd<float, false>(a, kinds, stream);
 }
 
 }  // namespace moe

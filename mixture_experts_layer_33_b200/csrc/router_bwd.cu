@@ -122,24 +122,24 @@ __device__ __forceinline__ void mma2(float (&c0)[4], float (&c1)[4], const uint3
 }
 
 // MT: E padded to 16 MT experts. Shared memory, bf16, rows padded by 8 to
-// spread ldmatrix rows over the banks: the x tile [TT][TC], the W_r columns
-// [16 MT][TC], dz as three terms [3][TT][16 MT]; the dx tile goes out
-// through the x tile's space.
+// spread ldmatrix rows over the banks: two x tiles [TT][TC] (the next one
+// is fetched while one is worked on), the W_r columns [16 MT][TC], dz as three
+// terms [3][TT][16 MT]; the dx tile goes out through its x tile's space.
 template <int MT> struct RbSmem {
   static constexpr int EP = 16 * MT;
   static constexpr int XP = TC + 8, ZP = EP + 8;
-  static constexpr size_t x = 0;
-  static constexpr size_t w = x + (size_t)TT * XP * 2;
+  static constexpr size_t x = 0;  // two tiles
+  static constexpr size_t w = x + (size_t)2 * TT * XP * 2;
   static constexpr size_t z = w + (size_t)EP * XP * 2;
   static constexpr size_t total = z + (size_t)3 * TT * ZP * 2;
 };
 
 template <int MT>
-__global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs a, int splits) {
+__global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs a, int splits, float *bias_part) {
   using S = RbSmem<MT>;
   constexpr int EP = S::EP, XP = S::XP, ZP = S::ZP;
   extern __shared__ __align__(16) uint8_t sm[];
-  __nv_bfloat16 *sx = reinterpret_cast<__nv_bfloat16 *>(sm + S::x);
+  __nv_bfloat16 *sx0 = reinterpret_cast<__nv_bfloat16 *>(sm + S::x);
   __nv_bfloat16 *sw = reinterpret_cast<__nv_bfloat16 *>(sm + S::w);
   __nv_bfloat16 *sz = reinterpret_cast<__nv_bfloat16 *>(sm + S::z);
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
@@ -149,14 +149,13 @@ __global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs
   const int c0 = blockIdx.x * TC, split = blockIdx.y;
   const int tiles = (a.T + TT - 1) / TT;
   const int t_lo = (int)((int64_t)tiles * split / splits), t_hi = (int)((int64_t)tiles * (split + 1) / splits);
-  const uint4 zero4 = make_uint4(0, 0, 0, 0);
   const bool want_w = a.dW_r != nullptr, want_x = dx != nullptr;
 
   if (want_x)
     for (int i = tid; i < EP * (TC / 8); i += kThreads) {
       const int e = i / (TC / 8), c = (i % (TC / 8)) * 8;
-      *reinterpret_cast<uint4 *>(sw + e * XP + c) =
-          (e < a.E && c0 + c < a.d) ? *reinterpret_cast<const uint4 *>(wr + (size_t)e * a.d + c0 + c) : zero4;
+      const bool in = e < a.E && c0 + c < a.d;
+      cp_async16(sw + e * XP + c, in ? wr + (size_t)e * a.d + c0 + c : wr, in);
     }
   float acc[MT][2][4];  // dW_r: all 16 MT experts x this warp's 16 columns
 #pragma unroll
@@ -165,34 +164,51 @@ __global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
-  float bias_sum = 0.f;  // thread e < E of column block 0
-
+  auto fetch_x = [&](int t) {
+    __nv_bfloat16 *o = sx0 + (t & 1) * TT * XP;
+    if (want_w && t < t_hi)
+      for (int i = tid; i < TT * (TC / 8); i += kThreads) {
+        const int r = t * TT + i / (TC / 8), c = (i % (TC / 8)) * 8;
+        const bool in = r < a.T && c0 + c < a.d;
+        cp_async16(o + (i / (TC / 8)) * XP + c, in ? x + (size_t)r * a.d + c0 + c : x, in);
+      }
+    cp_async_commit();
+  };
+  // dz of a tile, read a tile ahead.
+  constexpr int ZN = TT * EP / kThreads;
+  float zr[ZN];
+  auto fetch_z = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < ZN; ++i) {
+      const int r = t * TT + (tid + i * kThreads) / EP, e = (tid + i * kThreads) % EP;
+      zr[i] = (t < t_hi && r < a.T && e < a.E) ? a.dlogits[(size_t)r * a.E + e] : 0.f;
+    }
+  };
+  // A thread's zr are all of one expert (EP divides kThreads): column block 0
+  // sums them for dbias.
+  const bool want_b = a.dbias && blockIdx.x == 0;
+  float bias_sum = 0.f;
+  fetch_x(t_lo);
+  fetch_z(t_lo);
   for (int t = t_lo; t < t_hi; ++t) {
     const int s0 = t * TT;
-    __syncthreads();
-    if (want_w)
-      for (int i = tid; i < TT * (TC / 8); i += kThreads) {
-        const int r = i / (TC / 8), c = (i % (TC / 8)) * 8;
-        const bool in = s0 + r < a.T && c0 + c < a.d;
-        cp_async16(sx + r * XP + c, in ? x + (size_t)(s0 + r) * a.d + c0 + c : x, in);
-      }
-    for (int i = tid; i < TT * EP; i += kThreads) {
-      const int r = i / EP, e = i % EP;
-      const float z = (s0 + r < a.T && e < a.E) ? a.dlogits[(size_t)(s0 + r) * a.E + e] : 0.f;
-      const __nv_bfloat16 h = __float2bfloat16_rn(z);
-      const float z1 = z - __bfloat162float(h);
+    __nv_bfloat16 *sx = sx0 + (t & 1) * TT * XP;
+    __syncthreads();  // the last tile's dz and the other x tile have been read
+    fetch_x(t + 1);
+#pragma unroll
+    for (int i = 0; i < ZN; ++i) {
+      const int r = (tid + i * kThreads) / EP, e = (tid + i * kThreads) % EP;
+      const __nv_bfloat16 h = __float2bfloat16_rn(zr[i]);
+      const float z1 = zr[i] - __bfloat162float(h);
       const __nv_bfloat16 m = __float2bfloat16_rn(z1);
       sz[r * ZP + e] = h;
       sz[(TT + r) * ZP + e] = m;
       sz[(2 * TT + r) * ZP + e] = __float2bfloat16_rn(z1 - __bfloat162float(m));
+      bias_sum += zr[i];
     }
-    cp_async_commit();
-    cp_async_wait<0>();
+    fetch_z(t + 1);
+    cp_async_wait<1>();
     __syncthreads();
-    if (a.dbias && blockIdx.x == 0 && tid < a.E) {
-      const int n = min(TT, a.T - s0);
-      for (int r = 0; r < n; ++r) bias_sum += a.dlogits[(size_t)(s0 + r) * a.E + tid];
-    }
     if (want_w) {
       // dW_r[e][c] += sum_r dz[r][e] x[r][c]: A = dz^T (ldmatrix.trans on
       // [token][expert] rows), B = x (ldmatrix.trans on [token][column] rows).
@@ -262,96 +278,169 @@ __global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs
         }
       }
   }
-  if (a.dbias && blockIdx.x == 0 && tid < a.E)
-    a.part[(size_t)(a.dW_r ? splits : 0) * a.E * a.d + (size_t)split * a.E + tid] = bias_sum;
+  if (want_b) {
+    __shared__ float sb[kThreads];
+    sb[tid] = bias_sum;
+    __syncthreads();
+    if (tid < a.E) {
+      float t = 0.f;
+#pragma unroll
+      for (int k = 0; k < kThreads / EP; ++k) t += sb[k * EP + tid];
+      bias_part[(size_t)split * a.E + tid] = t;
+    }
+  }
 }
 
-// The same tiles in fp32 on CUDA cores (fp32 layers are small).
-__global__ void __launch_bounds__(kThreads) router_bwd_f32_kernel(RouterBwdArgs a, int splits) {
+// The same tiles in fp32 on CUDA cores (fp32 layers are small). A thread owns
+// a column and every fourth expert (EPT of them) or row. A tile's sums are
+// formed on their own and then added: shorter chains of rounding.
+template <int EPT>
+__global__ void __launch_bounds__(kThreads) router_bwd_f32_kernel(RouterBwdArgs a, int splits, float *bias_part) {
   extern __shared__ __align__(16) float fm[];
-  float *sx = fm;                      // [TT][FC]
-  float *sz = sx + TT * FC;            // [TT][E]
-  float *sw = sz + TT * a.E;           // [E][FC]
+  float *sx = fm;             // [TT][FC]
+  float *sw = sx + TT * FC;   // [E][FC]
+  float *sz = sw + a.E * FC;  // [TT][E]
   const float *x = static_cast<const float *>(a.x);
   const float *wr = static_cast<const float *>(a.W_r);
   float *dx = static_cast<float *>(a.dx);
   const int tid = threadIdx.x, c0 = blockIdx.x * FC, split = blockIdx.y;
   const int tiles = (a.T + TT - 1) / TT;
   const int t_lo = (int)((int64_t)tiles * split / splits), t_hi = (int)((int64_t)tiles * (split + 1) / splits);
-  const int col = tid % FC, lane4 = tid / FC;  // this thread's column, and every 4th row (expert) from lane4
+  const int col = tid % FC, lane4 = tid / FC;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   if (dx)
-    for (int i = tid; i < a.E * FC; i += kThreads)
-      sw[i] = c0 + i % FC < a.d ? wr[(size_t)(i / FC) * a.d + c0 + i % FC] : 0.f;
-  float acc[32];
+    for (int i = tid; i < a.E * (FC / 4); i += kThreads) {
+      const int e = i / (FC / 4), c = c0 + (i % (FC / 4)) * 4;
+      *reinterpret_cast<float4 *>(sw + i * 4) =
+          c < a.d ? *reinterpret_cast<const float4 *>(wr + (size_t)e * a.d + c) : zero;
+    }
+  const bool want_b = a.dbias && blockIdx.x == 0;
+  float bias_sum[16];  // experts warp + 8 i, in lane 0
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-  float bias_sum = 0.f;
+  for (int i = 0; i < 16; ++i) bias_sum[i] = 0.f;
+  float acc[EPT];
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) acc[i] = 0.f;
   for (int t = t_lo; t < t_hi; ++t) {
     const int s0 = t * TT;
     __syncthreads();
-    if (a.dW_r)
-      for (int i = tid; i < TT * FC; i += kThreads) {
-        const int r = s0 + i / FC, c = c0 + i % FC;
-        sx[i] = r < a.T && c < a.d ? x[(size_t)r * a.d + c] : 0.f;
-      }
-    for (int i = tid; i < TT * a.E; i += kThreads)
-      sz[i] = s0 + i / a.E < a.T ? a.dlogits[(size_t)s0 * a.E + i] : 0.f;
-    __syncthreads();
-    if (a.dbias && blockIdx.x == 0 && tid < a.E)
-      for (int r = 0; r < TT; ++r) bias_sum += sz[r * a.E + tid];
     if (a.dW_r) {
+      float4 v[TT * FC / 4 / kThreads];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int e = lane4 + 4 * i;
-        if (e >= a.E) break;
-        float v = 0.f;  // a tile's sum on its own, then into the running one: shorter chains of rounding
-        for (int r = 0; r < TT; ++r) v = fmaf(sz[r * a.E + e], sx[r * FC + col], v);
-        acc[i] += v;
+      for (int k = 0; k < TT * FC / 4 / kThreads; ++k) {
+        const int i = tid + k * kThreads, r = s0 + i / (FC / 4), c = c0 + (i % (FC / 4)) * 4;
+        v[k] = r < a.T && c < a.d ? *reinterpret_cast<const float4 *>(x + (size_t)r * a.d + c) : zero;
+      }
+#pragma unroll
+      for (int k = 0; k < TT * FC / 4 / kThreads; ++k) *reinterpret_cast<float4 *>(sx + (tid + k * kThreads) * 4) = v[k];
+    }
+    const int live = min(TT, a.T - s0) * a.E;
+#pragma unroll 4
+    for (int i = tid; i < TT * a.E; i += kThreads) sz[i] = i < live ? a.dlogits[(size_t)s0 * a.E + i] : 0.f;
+    __syncthreads();
+    if (want_b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int e = (tid >> 5) + 8 * i;
+        if (e < a.E) bias_sum[i] += warp_sum(sz[(tid & 31) * a.E + e] + sz[((tid & 31) + 32) * a.E + e]);
       }
     }
-    if (dx && c0 + col < a.d)
-      for (int r = lane4; r < TT && s0 + r < a.T; r += 4) {
-        float v = 0.f;
-        for (int e = 0; e < a.E; ++e) v = fmaf(sz[r * a.E + e], sw[e * FC + col], v);
-        dx[(size_t)(s0 + r) * a.d + c0 + col] = v;
+    if (a.dW_r) {
+      float v[EPT];
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) v[i] = 0.f;
+#pragma unroll 8
+      for (int r = 0; r < TT; ++r) {
+        const float xv = sx[r * FC + col];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i)
+          if (lane4 + 4 * i < a.E) v[i] = fmaf(sz[r * a.E + lane4 + 4 * i], xv, v[i]);
       }
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) acc[i] += v[i];
+    }
+    if (dx && c0 + col < a.d) {
+      float v[TT / 4];
+#pragma unroll
+      for (int i = 0; i < TT / 4; ++i) v[i] = 0.f;
+      for (int e = 0; e < a.E; ++e) {
+        const float w = sw[e * FC + col];
+#pragma unroll
+        for (int i = 0; i < TT / 4; ++i) v[i] = fmaf(sz[(lane4 + 4 * i) * a.E + e], w, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < TT / 4; ++i)
+        if (s0 + lane4 + 4 * i < a.T) dx[(size_t)(s0 + lane4 + 4 * i) * a.d + c0 + col] = v[i];
+    }
   }
   if (a.dW_r && c0 + col < a.d) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < EPT; ++i) {
       const int e = lane4 + 4 * i;
-      if (e >= a.E) break;
-      a.part[((size_t)split * a.E + e) * a.d + c0 + col] = acc[i];
+      if (e < a.E) a.part[((size_t)split * a.E + e) * a.d + c0 + col] = acc[i];
     }
   }
-  if (a.dbias && blockIdx.x == 0 && tid < a.E)
-    a.part[(size_t)(a.dW_r ? splits : 0) * a.E * a.d + (size_t)split * a.E + tid] = bias_sum;
-}
-
-// Sums the token ranges in order: dW_r [E, d], then dbias [E].
-__global__ void __launch_bounds__(kThreads) router_bwd_sum_kernel(const float *part, float *dW_r, float *dbias, int E,
-                                                                  int d, int splits) {
-  const int64_t nw = dW_r ? (int64_t)E * d : 0, n = nw + (dbias ? E : 0);
-  const float *pb = part + (size_t)splits * nw;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-    float v = 0.f;
-    if (i < nw) {
-#pragma unroll 8
-      for (int k = 0; k < splits; ++k) v += part[(size_t)k * nw + i];
-      dW_r[i] = v;
-    } else {
-      for (int k = 0; k < splits; ++k) v += pb[(size_t)k * E + (i - nw)];
-      dbias[i - nw] = v;
+  if (want_b && (tid & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = (tid >> 5) + 8 * i;
+      if (e < a.E) bias_part[(size_t)split * a.E + e] = bias_sum[i];
     }
   }
 }
 
-// Token ranges: enough CTAs (two per SM) with the columns, at least one tile
+// Sums the token ranges in order: dW_r [E, d], and dbias [E] in the last
+// block. 64 values by 16 slices of the list per CTA, the slices added in order.
+constexpr int kSumSlices = 16, kSumCols = 64, kSumThreads = kSumCols * kSumSlices / 4;
+__global__ void __launch_bounds__(kSumThreads) router_bwd_sum_kernel(const float *part, const float *bias_part,
+                                                                     float *dW_r, float *dbias, int E, int d,
+                                                                     int splits) {
+  __shared__ __align__(16) float sh[kSumSlices][kSumCols];
+  const int64_t nw = dW_r ? (int64_t)E * d : 0, c0 = (int64_t)blockIdx.x * kSumCols;
+  if (c0 >= nw) {  // dbias: a thread per expert and slice of the list
+    const int width = E <= 32 ? 32 : E <= 64 ? 64 : 128, slices = kSumThreads / width;
+    const int e = threadIdx.x % width, slice = threadIdx.x / width;
+    float t = 0.f;
+    if (e < E)
+#pragma unroll 16
+      for (int k = splits * slice / slices; k < splits * (slice + 1) / slices; ++k) t += bias_part[(size_t)k * E + e];
+    float *o = &sh[0][0];
+    o[threadIdx.x] = t;
+    __syncthreads();
+    if ((int)threadIdx.x >= E) return;
+    for (int k = 1; k < slices; ++k) t += o[k * width + threadIdx.x];
+    dbias[threadIdx.x] = t;
+    return;
+  }
+  const int quad = threadIdx.x % (kSumCols / 4), slice = threadIdx.x / (kSumCols / 4);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c0 + quad * 4 < nw) {
+    const int lo = splits * slice / kSumSlices, hi = splits * (slice + 1) / kSumSlices;
+#pragma unroll 4
+    for (int k = lo; k < hi; ++k) {
+      const float4 f = *reinterpret_cast<const float4 *>(part + (size_t)k * nw + c0 + quad * 4);
+      v.x += f.x;
+      v.y += f.y;
+      v.z += f.z;
+      v.w += f.w;
+    }
+  }
+  *reinterpret_cast<float4 *>(&sh[slice][quad * 4]) = v;
+  __syncthreads();
+  const int64_t i = c0 + threadIdx.x;
+  if (threadIdx.x >= kSumCols || i >= nw) return;
+  float t = 0.f;
+#pragma unroll
+  for (int k = 0; k < kSumSlices; ++k) t += sh[k][threadIdx.x];
+  dW_r[i] = t;
+}
+
+// Token ranges: as many CTAs with the columns as run at once (two per SM), at least one tile
 // each, and no more partial dW_r blocks than half the bytes of x.
 int token_splits(int T, int d, int E, int dtype) {
   const int cols = dtype == MOE_BF16 ? TC : FC, eb = dtype == MOE_BF16 ? 2 : 4;
   const int64_t tiles = (T + TT - 1) / TT, blocks = (d + cols - 1) / cols;
-  int64_t n = (2 * 148 + blocks - 1) / blocks;
+  int64_t n = 2 * 148 / blocks;
   const int64_t cap = (int64_t)T * eb / (8 * (int64_t)E);
   if (n > cap) n = cap;
   if (n > tiles) n = tiles;
@@ -359,21 +448,23 @@ int token_splits(int T, int d, int E, int dtype) {
 }
 
 template <int MT>
-int run_bf16(const RouterBwdArgs &a, int splits, cudaStream_t stream) {
+int run_bf16(const RouterBwdArgs &a, int splits, float *bias_part, cudaStream_t stream) {
   const dim3 grid((a.d + TC - 1) / TC, splits);
   MOE_CUDA_TRY(cudaFuncSetAttribute(router_bwd_bf16_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)RbSmem<MT>::total));
-  router_bwd_bf16_kernel<MT><<<grid, kThreads, RbSmem<MT>::total, stream>>>(a, splits);
+  router_bwd_bf16_kernel<MT><<<grid, kThreads, RbSmem<MT>::total, stream>>>(a, splits, bias_part);
   return last_launch_status();
 }
 
 }  // namespace
 
 size_t router_bwd_workspace_bytes(int T, int d, int E, int dtype) {
-  return ((size_t)E * d + E) * 4 * token_splits(T, d, E, dtype);
+  return (size_t)token_splits(T, d, E, dtype) * ((size_t)E * d + E) * 4;
 }
 
 int launch_router_bwd(const RouterBwdArgs &a, cudaStream_t stream) {
+  const int splits = token_splits(a.T, a.d, a.E, a.dtype);
+  float *bias_part = a.part + (size_t)splits * a.E * a.d;
   if (a.T > 0) {
     int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
     if (blocks > 8 * (int64_t)num_sms()) blocks = 8 * (int64_t)num_sms();
@@ -382,24 +473,27 @@ int launch_router_bwd(const RouterBwdArgs &a, cudaStream_t stream) {
     else if (a.E <= 64) router_dz_kernel<2><<<g, kThreads, 0, stream>>>(a);
     else router_dz_kernel<4><<<g, kThreads, 0, stream>>>(a);
   }
-  if (!a.dx && !a.dW_r && !a.dbias) return last_launch_status();
-  const int splits = token_splits(a.T, a.d, a.E, a.dtype);
-  int st = MOE_OK;
-  if (a.dtype == MOE_BF16) {
-    if (a.E <= 16) st = run_bf16<1>(a, splits, stream);
-    else if (a.E <= 32) st = run_bf16<2>(a, splits, stream);
-    else if (a.E <= 64) st = run_bf16<4>(a, splits, stream);
-    else st = run_bf16<8>(a, splits, stream);
-  } else {
-    const size_t smem = (size_t)(TT * FC + TT * a.E + a.E * FC) * 4;
-    MOE_CUDA_TRY(cudaFuncSetAttribute(router_bwd_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    router_bwd_f32_kernel<<<dim3((a.d + FC - 1) / FC, splits), kThreads, smem, stream>>>(a, splits);
-    st = last_launch_status();
+  int st = last_launch_status();
+  if (st == MOE_OK && (a.dx || a.dW_r || a.dbias)) {
+    if (a.dtype == MOE_BF16) {
+      if (a.E <= 16) st = run_bf16<1>(a, splits, bias_part, stream);
+      else if (a.E <= 32) st = run_bf16<2>(a, splits, bias_part, stream);
+      else if (a.E <= 64) st = run_bf16<4>(a, splits, bias_part, stream);
+      else st = run_bf16<8>(a, splits, bias_part, stream);
+    } else {
+      const size_t smem = (size_t)(TT * FC + TT * a.E + a.E * FC) * 4;
+      const auto kern = a.E <= 8    ? router_bwd_f32_kernel<2>
+                        : a.E <= 32 ? router_bwd_f32_kernel<8>
+                                    : router_bwd_f32_kernel<32>;
+      MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      kern<<<dim3((a.d + FC - 1) / FC, splits), kThreads, smem, stream>>>(a, splits, bias_part);
+      st = last_launch_status();
+    }
   }
   if (st != MOE_OK || (!a.dW_r && !a.dbias)) return st;
-  int64_t blocks = ((int64_t)a.E * a.d + a.E + kThreads - 1) / kThreads;
-  if (blocks > 1184) blocks = 1184;
-  router_bwd_sum_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a.part, a.dW_r, a.dbias, a.E, a.d, splits);
+  const int64_t blocks = (a.dW_r ? ((int64_t)a.E * a.d + kSumCols - 1) / kSumCols : 0) + (a.dbias ? 1 : 0);
+  router_bwd_sum_kernel<<<(unsigned)blocks, kSumThreads, 0, stream>>>(a.part, bias_part, a.dW_r, a.dbias, a.E, a.d,
+                                                                     splits);
   return last_launch_status();
 }
 

@@ -338,27 +338,42 @@ def forward_host(c: MoeConfig, x_host, W_r, W1, W2, y_host, ws, residual_host=No
 
 
 # ---------------------------------------------------------------- training
-def _grad_ptr(t, what, dtype, numel):
+def _grad_ptr(t, what, dtype, numel, dev):
     """Device pointer of a tensor argument of the gradients (None stays None): dtype, size,
     contiguity and device are checked, since a short buffer would be written past its end."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
-    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of {numel} elements, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != torch.cuda.current_device():  # -1: a host tensor
+    if t.get_device() != dev:  # -1: a host tensor
         raise ValueError(f"{what}: expected a tensor on the current CUDA device")
     return t.data_ptr()
 
 
-def _ws_ptr(ws):
-    return _grad_ptr(ws, "ws", torch.uint8, ws.numel())
-
-
 def _layer_dtype(c):
     return torch.bfloat16 if c.dtype == BF16 else torch.float32
+
+
+# The current stream's handle without a Stream object (1 us less per call) where torch has it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _assignments(c):
+    """moe_num_assignments of a config that the call itself will check."""
+    if c.routing != EXPERT_CHOICE:
+        return c.T * c.k
+    return c.T // c.group_size * c.E * c.capacity if c.group_size > 0 else 0
 
 
 def backward_workspace_size(c: MoeConfig) -> int:
@@ -382,33 +397,35 @@ def combine_backward(c: MoeConfig, dy, y_perm, sel, w, row_of, tok_ptr, tok_assi
                      dy_perm, dw, dev_status, ws, dconst=None, stream=None):
     """Gradient of ``combine`` (moe_combine_backward in include/moe.h). The token lists are
     accepted for symmetry with ``combine`` and not read."""
-    n, dt, f32, i32 = num_assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    n, dt, f32, i32 = _assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    dev = torch.cuda.current_device()
     nc = _n_const(c) * (3 if c.const_mix else 1) * c.d if c.n_heavy < c.E else 0
     _check(LIB.moe_combine_backward(
-        ctypes.byref(c), _grad_ptr(dy, "dy", dt, c.T * c.d), _grad_ptr(y_perm, "y_perm", dt, n * c.d),
-        _grad_ptr(sel, "sel", i32, n), _grad_ptr(w, "w", f32, n), _grad_ptr(row_of, "row_of", i32, n),
-        _grad_ptr(x, "x", dt, c.T * c.d), _grad_ptr(const_vecs, "const_vecs", dt, nc),
-        _grad_ptr(dy_perm, "dy_perm", dt, n * c.d), _grad_ptr(dw, "dw", f32, n),
-        _grad_ptr(dconst, "dconst", f32, nc), _grad_ptr(dev_status, "dev_status", i32, 1),
-        _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_combine_backward")
+        ctypes.byref(c), _grad_ptr(dy, "dy", dt, c.T * c.d, dev), _grad_ptr(y_perm, "y_perm", dt, n * c.d, dev),
+        _grad_ptr(sel, "sel", i32, n, dev), _grad_ptr(w, "w", f32, n, dev), _grad_ptr(row_of, "row_of", i32, n, dev),
+        _grad_ptr(x, "x", dt, c.T * c.d, dev), _grad_ptr(const_vecs, "const_vecs", dt, nc, dev),
+        _grad_ptr(dy_perm, "dy_perm", dt, n * c.d, dev), _grad_ptr(dw, "dw", f32, n, dev),
+        _grad_ptr(dconst, "dconst", f32, nc, dev), _grad_ptr(dev_status, "dev_status", i32, 1, dev),
+        _grad_ptr(ws, "ws", torch.uint8, ws.numel(), dev), ws.numel(), _raw_stream(stream, dev)), "moe_combine_backward")
 
 
 def dispatch_backward(c: MoeConfig, dx_perm, dy, sel, w, row_of, tok_ptr, tok_assign, x, const_vecs,
                       dx, dev_status, add=(), stream=None):
     """Gradient of ``dispatch``'s row gather and of the combine's x terms, with up to three
     [T, d] gradients ``add`` summed in the same pass (moe_dispatch_backward)."""
-    n, dt, f32, i32 = num_assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    n, dt, f32, i32 = _assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    dev = torch.cuda.current_device()
     nc = _n_const(c) * (3 if c.const_mix else 1) * c.d if c.n_heavy < c.E else 0
     if len(add) > 3:
         raise ValueError("add: at most three gradients")
-    adds = [_grad_ptr(t, "add", dt, c.T * c.d) for t in add] + [None] * (3 - len(add))
+    adds = [_grad_ptr(t, "add", dt, c.T * c.d, dev) for t in add] + [None] * (3 - len(add))
     _check(LIB.moe_dispatch_backward(
-        ctypes.byref(c), _grad_ptr(dx_perm, "dx_perm", dt, n * c.d), _grad_ptr(dy, "dy", dt, c.T * c.d),
-        _grad_ptr(sel, "sel", i32, n), _grad_ptr(w, "w", f32, n), _grad_ptr(row_of, "row_of", i32, n),
-        _grad_ptr(tok_ptr, "tok_ptr", i32, c.T + 1), _grad_ptr(tok_assign, "tok_assign", i32, n),
-        _grad_ptr(x, "x", dt, c.T * c.d), _grad_ptr(const_vecs, "const_vecs", dt, nc), *adds,
-        _grad_ptr(dx, "dx", dt, c.T * c.d), _grad_ptr(dev_status, "dev_status", i32, 1),
-        _stream(stream)), "moe_dispatch_backward")
+        ctypes.byref(c), _grad_ptr(dx_perm, "dx_perm", dt, n * c.d, dev), _grad_ptr(dy, "dy", dt, c.T * c.d, dev),
+        _grad_ptr(sel, "sel", i32, n, dev), _grad_ptr(w, "w", f32, n, dev), _grad_ptr(row_of, "row_of", i32, n, dev),
+        _grad_ptr(tok_ptr, "tok_ptr", i32, c.T + 1, dev), _grad_ptr(tok_assign, "tok_assign", i32, n, dev),
+        _grad_ptr(x, "x", dt, c.T * c.d, dev), _grad_ptr(const_vecs, "const_vecs", dt, nc, dev), *adds,
+        _grad_ptr(dx, "dx", dt, c.T * c.d, dev), _grad_ptr(dev_status, "dev_status", i32, 1, dev),
+        _raw_stream(stream, dev)), "moe_dispatch_backward")
 
 
 def router_backward(c: MoeConfig, x, W_r, probs, sel, w, dw, tok_ptr, tok_assign, dlogits,
@@ -416,36 +433,38 @@ def router_backward(c: MoeConfig, x, W_r, probs, sel, w, dw, tok_ptr, tok_assign
                     stream=None):
     """Gradient of the routing weights back through selection and softmax to the logits, and
     from there to the router's inputs (moe_router_backward)."""
-    n, dt, f32, i32 = num_assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    n, dt, f32, i32 = _assignments(c), _layer_dtype(c), torch.float32, torch.int32
+    dev = torch.cuda.current_device()
     te = c.T * c.E
     _check(LIB.moe_router_backward(
-        ctypes.byref(c), _grad_ptr(x, "x", dt, c.T * c.d), _grad_ptr(W_r, "W_r", dt, c.E * c.d),
-        _grad_ptr(probs, "probs", f32, te), _grad_ptr(sel, "sel", i32, n), _grad_ptr(w, "w", f32, n),
-        _grad_ptr(dw, "dw", f32, n), _grad_ptr(tok_ptr, "tok_ptr", i32, c.T + 1),
-        _grad_ptr(tok_assign, "tok_assign", i32, n), _grad_ptr(dprobs, "dprobs", f32, te),
-        _grad_ptr(dlogits, "dlogits", f32, te), _grad_ptr(dz_prev, "dz_prev", f32, te),
-        _grad_ptr(dbias, "dbias", f32, c.E), _grad_ptr(dW_r, "dW_r", f32, c.E * c.d),
-        _grad_ptr(dx, "dx", dt, c.T * c.d), _grad_ptr(dev_status, "dev_status", i32, 1),
-        _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_router_backward")
+        ctypes.byref(c), _grad_ptr(x, "x", dt, c.T * c.d, dev), _grad_ptr(W_r, "W_r", dt, c.E * c.d, dev),
+        _grad_ptr(probs, "probs", f32, te, dev), _grad_ptr(sel, "sel", i32, n, dev), _grad_ptr(w, "w", f32, n, dev),
+        _grad_ptr(dw, "dw", f32, n, dev), _grad_ptr(tok_ptr, "tok_ptr", i32, c.T + 1, dev),
+        _grad_ptr(tok_assign, "tok_assign", i32, n, dev), _grad_ptr(dprobs, "dprobs", f32, te, dev),
+        _grad_ptr(dlogits, "dlogits", f32, te, dev), _grad_ptr(dz_prev, "dz_prev", f32, te, dev),
+        _grad_ptr(dbias, "dbias", f32, c.E, dev), _grad_ptr(dW_r, "dW_r", f32, c.E * c.d, dev),
+        _grad_ptr(dx, "dx", dt, c.T * c.d, dev), _grad_ptr(dev_status, "dev_status", i32, 1, dev),
+        _grad_ptr(ws, "ws", torch.uint8, ws.numel(), dev), ws.numel(), _raw_stream(stream, dev)), "moe_router_backward")
 
 
 def grouped_mlp_backward(c: MoeConfig, x_perm, offsets, W1, W2, dy_perm, x, Ws1, Ws2, dy_shared,
                          dev_status, ws, dx_perm=None, dW1=None, dW2=None, dx_shared=None,
                          dWs1=None, dWs2=None, stream=None):
     """Gradient of ``grouped_mlp``; any output may be left out (moe_grouped_mlp_backward)."""
-    n, dt, i32 = num_assignments(c), _layer_dtype(c), torch.int32
+    n, dt, i32 = _assignments(c), _layer_dtype(c), torch.int32
+    dev = torch.cuda.current_device()
     up, hs = (2 * c.h if c.act == SWIGLU else c.h), c.n_shared * c.h_shared
     n1, n2, ns, td = c.n_heavy * up * c.d, c.n_heavy * c.h * c.d, hs * c.d, c.T * c.d
     _check(LIB.moe_grouped_mlp_backward(
-        ctypes.byref(c), _grad_ptr(x_perm, "x_perm", dt, n * c.d),
-        _grad_ptr(offsets, "offsets", i32, c.n_heavy + 1), _grad_ptr(W1, "W1", dt, n1),
-        _grad_ptr(W2, "W2", dt, n2), _grad_ptr(dy_perm, "dy_perm", dt, n * c.d),
-        _grad_ptr(x, "x", dt, td), _grad_ptr(Ws1, "Ws1", dt, ns), _grad_ptr(Ws2, "Ws2", dt, ns),
-        _grad_ptr(dy_shared, "dy_shared", dt, td), _grad_ptr(dx_perm, "dx_perm", dt, n * c.d),
-        _grad_ptr(dW1, "dW1", dt, n1), _grad_ptr(dW2, "dW2", dt, n2),
-        _grad_ptr(dx_shared, "dx_shared", dt, td), _grad_ptr(dWs1, "dWs1", dt, ns),
-        _grad_ptr(dWs2, "dWs2", dt, ns), _grad_ptr(dev_status, "dev_status", i32, 1),
-        _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_grouped_mlp_backward")
+        ctypes.byref(c), _grad_ptr(x_perm, "x_perm", dt, n * c.d, dev),
+        _grad_ptr(offsets, "offsets", i32, c.n_heavy + 1, dev), _grad_ptr(W1, "W1", dt, n1, dev),
+        _grad_ptr(W2, "W2", dt, n2, dev), _grad_ptr(dy_perm, "dy_perm", dt, n * c.d, dev),
+        _grad_ptr(x, "x", dt, td, dev), _grad_ptr(Ws1, "Ws1", dt, ns, dev), _grad_ptr(Ws2, "Ws2", dt, ns, dev),
+        _grad_ptr(dy_shared, "dy_shared", dt, td, dev), _grad_ptr(dx_perm, "dx_perm", dt, n * c.d, dev),
+        _grad_ptr(dW1, "dW1", dt, n1, dev), _grad_ptr(dW2, "dW2", dt, n2, dev),
+        _grad_ptr(dx_shared, "dx_shared", dt, td, dev), _grad_ptr(dWs1, "dWs1", dt, ns, dev),
+        _grad_ptr(dWs2, "dWs2", dt, ns, dev), _grad_ptr(dev_status, "dev_status", i32, 1, dev),
+        _grad_ptr(ws, "ws", torch.uint8, ws.numel(), dev), ws.numel(), _raw_stream(stream, dev)), "moe_grouped_mlp_backward")
 
 
 # ------------------------------------------------------------- block norms
@@ -459,7 +478,7 @@ def make_norm_config(cfg) -> MoeNormConfig:
                          float(cfg.get("res_scale", 1.0)))
 
 
-def _cond_ptrs(n: MoeNormConfig, named, dtype):
+def _cond_ptrs(n: MoeNormConfig, named, dtype, dev):
     """Pointers and the common row stride of condition tensors [rows, d]: chunks of one
     projection, so rows may be further apart than d."""
     rows = -(-n.T // n.group_size) if n.group_size else 1
@@ -471,7 +490,7 @@ def _cond_ptrs(n: MoeNormConfig, named, dtype):
         if t.dtype != dtype or tuple(t.shape) != (rows, n.d) or t.stride(1) != 1:
             raise ValueError(f"{what}: expected {dtype} rows [{rows}, {n.d}], got {t.dtype} "
                              f"{tuple(t.shape)} with strides {t.stride()}")
-        if t.get_device() != torch.cuda.current_device():
+        if t.get_device() != dev:
             raise ValueError(f"{what}: expected a tensor on the current CUDA device")
         if rows > 1:
             if any(p is not None for p in ptrs) and t.stride(0) != stride:
@@ -485,14 +504,14 @@ def block_norm(n: MoeNormConfig, h, x, y=None, z=None, post_gamma=None, gate=Non
                pre_beta=None, scale=None, shift=None, stream=None):
     """y = res_scale x + gate N_post(h) post_gamma; z = (N_pre(y) pre_gamma + pre_beta)(1 + scale)
     + shift (moe_block_norm): the end of one block and the start of the next in one pass."""
-    dt = _layer_dtype(n)
+    dt, dev = _layer_dtype(n), torch.cuda.current_device()
     td = n.T * n.d
-    (gp, scp, shp), stride = _cond_ptrs(n, (("gate", gate), ("scale", scale), ("shift", shift)), dt)
+    (gp, scp, shp), stride = _cond_ptrs(n, (("gate", gate), ("scale", scale), ("shift", shift)), dt, dev)
     _check(LIB.moe_block_norm(
-        ctypes.byref(n), _grad_ptr(h, "h", dt, td), _grad_ptr(x, "x", dt, td),
-        _grad_ptr(post_gamma, "post_gamma", dt, n.d), gp, _grad_ptr(pre_gamma, "pre_gamma", dt, n.d),
-        _grad_ptr(pre_beta, "pre_beta", dt, n.d), scp, shp, stride, _grad_ptr(y, "y", dt, td),
-        _grad_ptr(z, "z", dt, td), _stream(stream)), "moe_block_norm")
+        ctypes.byref(n), _grad_ptr(h, "h", dt, td, dev), _grad_ptr(x, "x", dt, td, dev),
+        _grad_ptr(post_gamma, "post_gamma", dt, n.d, dev), gp, _grad_ptr(pre_gamma, "pre_gamma", dt, n.d, dev),
+        _grad_ptr(pre_beta, "pre_beta", dt, n.d, dev), scp, shp, stride, _grad_ptr(y, "y", dt, td, dev),
+        _grad_ptr(z, "z", dt, td, dev), _raw_stream(stream, dev)), "moe_block_norm")
 
 
 def block_norm_workspace_size(n: MoeNormConfig) -> int:
@@ -511,19 +530,19 @@ def block_norm_backward(n: MoeNormConfig, h, y, dz, dy, ws, dh=None, dx=None, po
                         dgate=None, dpre_gamma=None, dpre_beta=None, dscale=None, dshift=None,
                         stream=None):
     """Gradient of ``block_norm`` from dz and dy (moe_block_norm_backward)."""
-    dt, f32 = _layer_dtype(n), torch.float32
+    dt, f32, dev = _layer_dtype(n), torch.float32, torch.cuda.current_device()
     td = n.T * n.d
-    (gp, scp), stride = _cond_ptrs(n, (("gate", gate), ("scale", scale)), dt)
+    (gp, scp), stride = _cond_ptrs(n, (("gate", gate), ("scale", scale)), dt, dev)
     (dgp, dscp, dshp), dstride = _cond_ptrs(
-        n, (("dgate", dgate), ("dscale", dscale), ("dshift", dshift)), f32)
+        n, (("dgate", dgate), ("dscale", dscale), ("dshift", dshift)), f32, dev)
     _check(LIB.moe_block_norm_backward(
-        ctypes.byref(n), _grad_ptr(h, "h", dt, td), _grad_ptr(y, "y", dt, td),
-        _grad_ptr(post_gamma, "post_gamma", dt, n.d), gp, _grad_ptr(pre_gamma, "pre_gamma", dt, n.d),
-        _grad_ptr(pre_beta, "pre_beta", dt, n.d), scp, stride, _grad_ptr(dz, "dz", dt, td),
-        _grad_ptr(dy, "dy", dt, td), _grad_ptr(dh, "dh", dt, td), _grad_ptr(dx, "dx", dt, td),
-        _grad_ptr(dpost_gamma, "dpost_gamma", f32, n.d), dgp,
-        _grad_ptr(dpre_gamma, "dpre_gamma", f32, n.d), _grad_ptr(dpre_beta, "dpre_beta", f32, n.d),
-        dscp, dshp, dstride, _ws_ptr(ws), ws.numel(), _stream(stream)), "moe_block_norm_backward")
+        ctypes.byref(n), _grad_ptr(h, "h", dt, td, dev), _grad_ptr(y, "y", dt, td, dev),
+        _grad_ptr(post_gamma, "post_gamma", dt, n.d, dev), gp, _grad_ptr(pre_gamma, "pre_gamma", dt, n.d, dev),
+        _grad_ptr(pre_beta, "pre_beta", dt, n.d, dev), scp, stride, _grad_ptr(dz, "dz", dt, td, dev),
+        _grad_ptr(dy, "dy", dt, td, dev), _grad_ptr(dh, "dh", dt, td, dev), _grad_ptr(dx, "dx", dt, td, dev),
+        _grad_ptr(dpost_gamma, "dpost_gamma", f32, n.d, dev), dgp,
+        _grad_ptr(dpre_gamma, "dpre_gamma", f32, n.d, dev), _grad_ptr(dpre_beta, "dpre_beta", f32, n.d, dev),
+        dscp, dshp, dstride, _grad_ptr(ws, "ws", torch.uint8, ws.numel(), dev), ws.numel(), _raw_stream(stream, dev)), "moe_block_norm_backward")
 
 
 class MoELayer:

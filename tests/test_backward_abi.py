@@ -187,16 +187,16 @@ def test_block_norm_backward_refusals(m):
 def test_binding_refuses_wrong_tensors(m, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     p = m._grad_ptr
-    assert p(None, "t", torch.float32, 4) is None
+    assert p(None, "t", torch.float32, 4, 0) is None
     with pytest.raises(TypeError):
-        p([1.0], "t", torch.float32, 1)
+        p([1.0], "t", torch.float32, 1, 0)
     for bad in (torch.zeros(4, dtype=torch.float64), torch.zeros(3), torch.zeros(4, 2)[:, 0], torch.zeros(4)):
         with pytest.raises(ValueError):  # type, size, layout, and (the last) a host tensor
-            p(bad, "t", torch.float32, 4)
+            p(bad, "t", torch.float32, 4, 0)
     n = norm(m)
     for bad in (torch.zeros(3, 256, dtype=torch.bfloat16), torch.zeros(4, 256), torch.zeros(4, 256, dtype=torch.bfloat16),
                 torch.zeros(256, 4, dtype=torch.bfloat16).t()):
         with pytest.raises(ValueError):
-            m._cond_ptrs(n, (("gate", bad),), torch.bfloat16)
+            m._cond_ptrs(n, (("gate", bad),), torch.bfloat16, 0)
     with pytest.raises(ValueError):
         m.dispatch_backward(cfg(m), None, None, None, None, None, None, None, None, None, None, None, add=[None] * 4)
