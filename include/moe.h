@@ -77,8 +77,9 @@ enum moe_status {
 #define MOE_DEV_BAD_TOKEN 2u  /* a selected token id outside [0, T) */
 #define MOE_DEV_TIMEOUT 4u    /* a bounded wait inside a kernel expired */
 #define MOE_DEV_OVERFLOW 8u   /* more rows than the caller's buffers hold */
-#define MOE_DEV_BAD_INDEX 16u /* MOE_DEBUG builds: a caller-supplied row offset, row or
-                                 token-list index out of range (skipped) */
+#define MOE_DEV_BAD_INDEX 16u /* a caller-supplied row offset, row or token-list index out of
+                                 range (skipped): the forward's in MOE_DEBUG builds, rows and
+                                 token lists of the backward entry points in every build */
 
 enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 };
 enum moe_routing { MOE_TOKEN_TOPK = 0, MOE_EXPERT_CHOICE = 1, MOE_DES_VOTE = 2, MOE_DES_SEQ = 3 };
@@ -561,9 +562,8 @@ MOE_API int moe_router_backward(const moe_config *cfg, const void *x, const void
  *   dx_perm   [n_assign, d] out     rows past offsets[n_heavy] left as they were
  *   dW1, dW2, dWs1, dWs2            shaped and typed like the weights
  *   dx_shared [T, d] out
- * Any output may be NULL: what only it needs is not computed. Inputs that
- * no given output needs may be NULL too when all routed (or all shared)
- * outputs are.
+ * Any output may be NULL: its product is left out. When all routed (or all
+ * shared) outputs are NULL their inputs may be too.
  */
 MOE_API int moe_grouped_mlp_backward(const moe_config *cfg, const void *x_perm,
                              const int32_t *offsets, const void *W1, const void *W2,
@@ -584,7 +584,7 @@ MOE_API int moe_grouped_mlp_backward(const moe_config *cfg, const void *x_perm,
  * (MOE_NORM_LAYER) or v / sqrt(mean v^2 + eps) (MOE_NORM_RMS). y is rounded
  * once; z is formed from the unrounded y. A missing weight or condition
  * (NULL) is 1 or 0.
- *   T, d        tokens and width (d a multiple of 8, at most 8192)
+ *   T, d        tokens (at most 2^30) and width (a multiple of 8, at most 8192)
  *   group_size  tokens that share a condition row; 0: one row for all
  *   pre_kind, post_kind, eps (> 0), res_scale
  */

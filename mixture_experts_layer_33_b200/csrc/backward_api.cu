@@ -71,7 +71,7 @@ int check_norm(const moe_norm_config *c) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->dtype != MOE_BF16 && c->dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
   if (c->T < 0 || c->d < 8 || c->d % 8 != 0 || c->group_size < 0) return MOE_ERR_INVALID_ARG;
-  if (c->d > kNormMaxWidth) return MOE_ERR_UNSUPPORTED;
+  if (c->d > kNormMaxWidth || c->T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   for (int k : {c->pre_kind, c->post_kind})
     if (k != MOE_NORM_NONE && k != MOE_NORM_LAYER && k != MOE_NORM_RMS) return MOE_ERR_INVALID_ARG;
   if (!(c->eps > 0.f) || !isfinite(c->eps) || !isfinite(c->res_scale)) return MOE_ERR_INVALID_ARG;

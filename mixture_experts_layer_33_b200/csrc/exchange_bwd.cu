@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(ExchangeBwdArgs a
 // thread adds the listed rows into the 8 columns it owns. Chunks are summed
 // by a second launch in chunk order.
 __host__ __device__ inline int const_chunks(int64_t n_assign, int n_const) {
-  // 16 assignments or more to a chunk (a chunk also costs its partial sums'
+  // 48 assignments or more to a chunk (a chunk also costs its partial sums'
   // traffic), up to four CTAs per SM over the constant experts.
-  const int64_t want = (n_assign + 15) / 16, cap = 592 / (n_const > 0 ? n_const : 1);
+  const int64_t want = (n_assign + 47) / 48, cap = 592 / (n_const > 0 ? n_const : 1);
   return (int)(want < 1 ? 1 : want < cap ? want : cap < 1 ? 1 : cap);
 }
 

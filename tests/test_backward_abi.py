@@ -133,7 +133,7 @@ def block_norm(m, n, **kw):
 
 
 @pytest.mark.parametrize("field,value,code", [
-    ("T", -1, BAD), ("d", 12, BAD), ("d", 0, BAD), ("d", 8200, UNSUPPORTED), ("dtype", 5, BAD), ("group_size", -1, BAD),
+    ("T", -1, BAD), ("T", (1 << 30) + 1, UNSUPPORTED), ("d", 12, BAD), ("d", 0, BAD), ("d", 8200, UNSUPPORTED), ("dtype", 5, BAD), ("group_size", -1, BAD),
     ("pre_kind", 3, BAD), ("post_kind", -1, BAD), ("eps", 0.0, BAD), ("eps", -1.0, BAD), ("eps", float("nan"), BAD),
     ("eps", float("inf"), BAD), ("res_scale", float("nan"), BAD)])
 def test_norm_config_refusals(m, field, value, code):
