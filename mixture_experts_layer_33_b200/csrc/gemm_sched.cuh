@@ -1,6 +1,7 @@
-// The tile schedule of the persistent grouped GEMMs: a table of row tiles
-// over (problem, row group) entries and the order a CTA or CTA pair runs
-// them in.
+// The tile schedule of the MLP gradient's persistent GEMMs over ragged rows: a
+// table of row tiles over (problem, row group) entries and the order a CTA
+// pair runs them in. The forward's GEMM (gemm_sm100.cu) keeps its own, on
+// whose source its committed traffic captures are keyed.
 #pragma once
 
 #include "common.cuh"

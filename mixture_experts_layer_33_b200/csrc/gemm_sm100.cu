@@ -36,7 +36,6 @@
 #include <vector>
 
 #include "common.cuh"
-#include "gemm_sched.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
 
@@ -45,8 +44,11 @@ namespace {
 
 using namespace tc;
 
+constexpr int BM = 128;
+constexpr int BK = 64;  // 64 bf16 = 128 bytes = one swizzle atom row
 constexpr int kEpiWarps = 8;                    // two per TMEM lane quadrant
 constexpr int kThreads = 64 + 32 * kEpiWarps;   // producer warp, MMA warp, epilogue warps
+constexpr int kMaxEntries = 2 * kMaxLayerExperts + 2;  // (problem, group) entries of a launch
 constexpr uint32_t kStageOutBytes = 32 * 32 * 2;           // an epilogue warp's 32 x 32 bf16 staging tile
 
 struct ProbDev {
@@ -67,6 +69,77 @@ struct ParamsDev {
   ProbDev pr[2];
   int32_t *status;
 };
+
+struct Sched {
+  int n_entries;
+  int total_tiles;
+  int prob_end[2];  // tiles of problem 0 are [0, prob_end[0]), problem 1 [prob_end[0], prob_end[1])
+  int tile_start[kMaxEntries + 1];
+  int prob[kMaxEntries];
+  int group[kMaxEntries];
+  int row0[kMaxEntries];
+  int row_end[kMaxEntries];
+};
+
+// The tiles one CTA pair runs, in order. Every tile of a problem costs the
+// same (its K blocks), so with two problems of different K a round-robin
+// deal can leave some pairs a whole long tile behind the others, which
+// matters when there are few tiles per pair. Instead the longer problem's
+// tiles are dealt round-robin first, and then each tile of the shorter
+// problem, in order, goes to the pair that becomes free first (list
+// scheduling with known durations, equal free times to the lower id). After
+// the long deal the pairs below r hold one long tile more than the rest, so
+// pair c's m-th short slot starts at a known time and its rank in the
+// merged (start time, pair id) order, which is the short tile it gets, has a
+// closed form. Tiles close in the order still run at about the same time,
+// as with round-robin. Equal K (or one problem) is round-robin over the
+// whole table.
+struct TileSeq {
+  int c, P;
+  int startA, nA, startB, nB;
+  int a, b, r, plo;
+  int j, m;
+
+  __device__ void init(const Sched &s, int kb0, int kb1, int n_probs, int id, int n) {
+    c = id; P = n; j = id; m = 0;
+    const int n0 = s.prob_end[0], n1 = n_probs > 1 ? s.prob_end[1] - s.prob_end[0] : 0;
+    if (n1 == 0 || n0 == 0 || kb0 == kb1) {
+      startA = 0; nA = s.total_tiles; startB = 0; nB = 0; a = b = 1;
+    } else if (kb0 > kb1) {
+      startA = 0; nA = n0; a = kb0; startB = n0; nB = n1; b = kb1;
+    } else {
+      startA = n0; nA = n1; a = kb1; startB = 0; nB = n0; b = kb0;
+    }
+    r = nA % P;
+    plo = P - r;
+  }
+  // Next tile of this pair, or -1.
+  __device__ int next() {
+    if (j < nA) { const int t = startA + j; j += P; return t; }
+    if (nB == 0) return -1;
+    int pos;
+    if (c >= r) {  // free at m*b (relative to the lower load after the long deal)
+      const int t = m * b;
+      const int hi_before = t >= a ? (t - a) / b + 1 : 0;  // slots of the r loaded pairs at times <= t
+      pos = m * plo + (c - r) + r * hi_before;
+    } else {       // free at a + m*b
+      const int t = a + m * b;
+      const int lo_before = (t + b - 1) / b;               // slots of the others at times < t
+      pos = m * r + c + plo * lo_before;
+    }
+    ++m;
+    return pos < nB ? startB + pos : -1;
+  }
+};
+
+__device__ __forceinline__ int find_entry(const Sched &s, int t) {
+  int lo = 0, hi = s.n_entries - 1;
+  while (lo < hi) {
+    int mid = (lo + hi + 1) >> 1;
+    if (s.tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
 
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
@@ -678,9 +751,30 @@ grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_
 }
 
 // ------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once (a function-local static
+// is initialised once, safely under concurrent first calls); null if the
+// driver does not provide it.
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFn>(ptr);
+    return static_cast<EncodeTiledFn>(nullptr);
+  }();
+  return fn;
+}
+
 // 2D bf16 tensor [rows, cols] (cols contiguous), box {64, box_rows}, 128B swizzle.
 bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int box_rows) {
-  const TensorMapEncoder fn = tensor_map_encoder();
+  EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)(rows > 0 ? rows : 1)};
   cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
@@ -698,7 +792,7 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int b
 bool make_out_map(CUtensorMap *m, const GemmProblem &q) {
   if ((reinterpret_cast<uintptr_t>(q.out) & 15u) != 0 || (q.ld_out * 2) % 16 != 0 || q.a_rows <= 0)
     return false;
-  const TensorMapEncoder fn = tensor_map_encoder();
+  EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)q.N, (cuuint64_t)q.a_rows};
   cuuint64_t strides[1] = {(cuuint64_t)q.ld_out * 2};
@@ -832,21 +926,6 @@ int run_tc_pair(const GemmProblem *probs, int n_probs, int32_t *status, cudaStre
 }
 
 }  // namespace
-
-// Looked up once (a function-local static is initialised once, safely under
-// concurrent first calls).
-TensorMapEncoder tensor_map_encoder() {
-  static const TensorMapEncoder fn = [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<TensorMapEncoder>(ptr);
-    return static_cast<TensorMapEncoder>(nullptr);
-  }();
-  return fn;
-}
 
 bool make_tma_2d_bf16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int box_rows) {
   return make_map(map, ptr, rows, cols, box_rows);

@@ -223,13 +223,6 @@ int launch_grouped_gemm_bf16(const GemmProblem *probs, int n_probs, int act,
                              bool out_f32, int32_t *dev_status,
                              cudaStream_t stream, const GemmProblem *also = nullptr);
 
-// The driver's tensor-map encoder, or null if the driver does not provide it.
-typedef CUresult (*TensorMapEncoder)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                     const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                     const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-TensorMapEncoder tensor_map_encoder();
-
 // 2-D bf16 TMA descriptor [rows, cols] (cols contiguous), box {64, box_rows},
 // 128-byte swizzle, zero fill outside the tensor.
 bool make_tma_2d_bf16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int box_rows);

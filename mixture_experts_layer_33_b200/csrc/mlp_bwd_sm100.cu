@@ -801,6 +801,25 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
 }
 
 // ------------------------------------------------------------ host side
+typedef CUresult (*TensorMapEncoder)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                     const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                     CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                     CUtensorMapFloatOOBfill);
+// The driver's tensor-map encoder, looked up once (a function-local static is
+// initialised once, safely under concurrent first calls); null if the driver
+// does not provide it.
+TensorMapEncoder tensor_map_encoder() {
+  static const TensorMapEncoder fn = [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<TensorMapEncoder>(ptr);
+    return static_cast<TensorMapEncoder>(nullptr);
+  }();
+  return fn;
+}
+
 // bf16 tensor [z, rows, cols] (z = 0: 2-D), box {bx, by}, swizzled by the
 // box's row: 128 bytes (64 columns) or 64 (32 columns).
 bool make_map(CUtensorMap *m, const void *ptr, int64_t cols, int64_t rows, int64_t z, int bx, int by, bool store) {
