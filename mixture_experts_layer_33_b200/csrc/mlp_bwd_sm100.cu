@@ -735,26 +735,39 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * BN);
+      auto release = [&] {  // the accumulator may be overwritten
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8 * acc);
+      };
       if (RAGGED_K) {
-        // dW's rows end with its tensor, where the TMA store clips them.
-#pragma unroll 1
-        for (int c = c_lo; c < c_lo + half; c += 64) {
-          const int col = t.n0 + c;
-          if (col >= pr.N || wrow0 >= pr.M) break;
-          float v[2][32];
-          if (t.nkb > 0) {
-            tmem_ld64(taddr + c, v);
+        // The accumulator goes into registers and is handed back before the
+        // stores: small groups' tiles are little else, and MMA, epilogue and
+        // the two signals between them would otherwise take turns. dW's rows
+        // end with its tensor, where the TMA store clips them.
+        float v[2][2][32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (t.nkb > 0 && 64 * k < half) {
+            tmem_ld64(taddr + c_lo + 64 * k, v[k]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0.f;
+            for (int i = 0; i < 32; ++i) v[k][0][i] = v[k][1][i] = 0.f;
           }
-          stage_begin(lane);
-          stage_row(v, stg, lane);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&tm.o[t.pi], col, wrow0, t.g, stg);
-            bulk_commit();
+        }
+        if (t.nkb > 0) release();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = t.n0 + c_lo + 64 * k;
+          if (64 * k < half && col < pr.N && wrow0 < pr.M) {
+            stage_begin(lane);
+            stage_row(v[k], stg, lane);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tm.o[t.pi], col, wrow0, t.g, stg);
+              bulk_commit();
+            }
           }
         }
       } else {
@@ -782,9 +795,7 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
         }
       }
       if (t.nkb > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8 * acc);
+        if (!RAGGED_K) release();
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
     }
