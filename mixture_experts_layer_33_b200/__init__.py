@@ -1,4 +1,4 @@
-"""B200-native (sm_100a) MoE-layer forward pass.
+"""B200-native (sm_100a) MoE layer: forward pass, gradients, block norms.
 
 The compute path is ``libmoe.so`` (hand-written CUDA for sm_100a behind the
 C ABI in ``include/moe.h``); ``mixture_experts_layer_33_b200.moe`` is its

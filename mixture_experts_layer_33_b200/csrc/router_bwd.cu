@@ -17,7 +17,9 @@
 // bf16 layers multiply on bf16 mma.sync (as the router's forward does: N = E
 // is far too narrow for a tcgen05 tile). dz is fp32 and enters as the sum of
 // three bf16 terms (8 mantissa bits each, 24 in all), so the products keep
-// fp32 accuracy while x and W_r are exact.
+// fp32 accuracy while x and W_r are exact. 8192 x 1152, 19 experts: 6.5 + 18 +
+// 4 us, 28.7 back to back, where a copy of x takes 13; the middle launch keeps
+// the tensor pipe 44 % and L1 65 % busy (three terms, experts padded to 32).
 #include "backward.h"
 #include "mma_sync.cuh"
 
