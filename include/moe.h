@@ -564,6 +564,8 @@ MOE_API int moe_router_backward(const moe_config *cfg, const void *x, const void
  *   dx_shared [T, d] out
  * Any output may be NULL: its product is left out. When all routed (or all
  * shared) outputs are NULL their inputs may be too.
+ * No output may overlap an input or another output: the products that read
+ * the inputs and those that write the outputs may run at the same time.
  */
 MOE_API int moe_grouped_mlp_backward(const moe_config *cfg, const void *x_perm,
                              const int32_t *offsets, const void *W1, const void *W2,

@@ -18,7 +18,8 @@
 //              holds in fp32 registers; when dH is done it stores the
 //              product. The next tile's U overlaps that second half.
 //   dX         rows ragged, K = hidden width, two accumulators in turn.
-//   dW         both weight gradients (K = the group's rows) in one launch.
+//   dW         both weight gradients (K = the group's rows) in one launch;
+//              small groups' dX and dW side by side in one.
 // DiT-MoE-XL (8 experts that share 16384 rows, two shared experts of 8192
 // each, 1152 x 4608, 1.74 TFLOP): 525-548 + 222-247 + 540-562 us launched
 // apart (1270-1325, 1410-1565 and 1240-1290 TFLOP/s of a 1660 burst peak),
@@ -475,6 +476,15 @@ struct GemmMaps {
   CUtensorMap a[kMaxProbs], b[kMaxProbs], o[kMaxProbs];
 };
 
+// dX and dW side by side: the first x_pairs pairs run dX.
+struct BothMaps {
+  GemmMaps x, w;
+};
+struct BothParams {
+  GemmParams x, w;
+  int x_pairs;
+};
+
 struct Tile {
   int pi, g, m0, n0, nw;  // m0: dX's first row, dW's first output row; nw: columns of the MMA
   int lo, hi;             // the group's rows (dX: row_end in hi)
@@ -537,9 +547,9 @@ template <> struct Tiles<true> {
 // dX's tile table takes that space.
 constexpr uint32_t staging_bytes(bool ragged_k) { return ragged_k ? 2 * kStgBytes : kStgBytes; }
 
+// One CTA's part of pair `id` of `n`.
 template <bool RAGGED_K>
-__global__ void __launch_bounds__(kThreads + (RAGGED_K ? 32 : 0), 1)
-mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__ GemmParams p) {
+__device__ __forceinline__ void pair_gemm(const GemmMaps &tm, const GemmParams &p, int id, int n) {
   constexpr uint32_t IDESC0 = kMajorB | (RAGGED_K ? kMajorA : 0u);
   constexpr uint32_t IDESC_W = idesc_bf16_f32(BMP, BN) | IDESC0, IDESC_N = idesc_bf16_f32(BMP, BN / 2) | IDESC0;
 
@@ -548,14 +558,16 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   // dX: the table of row tiles; dW: the routed groups' row offsets.
+  // dX's table lies behind its staging tiles.
   struct Offsets { int at[kMaxLayerExperts + 1]; };
-  __shared__ typename std::conditional<RAGGED_K, Offsets, Sched>::type table;
+  __shared__ Offsets offsets;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sA = smem_u32(base), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * B_BYTES;
+  Sched &sched = *reinterpret_cast<Sched *>(base + STAGES * (A_BYTES + B_BYTES) + kEpiWarps * kStgBytes);
   const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
   const uint32_t tfull0 = smem_u32(&bars[2 * STAGES]), tempty0 = smem_u32(&bars[2 * STAGES + 2]);
   const uint32_t drain = smem_u32(&bars[2 * STAGES + 4]), tail0 = smem_u32(&bars[2 * STAGES + 5]);
@@ -590,13 +602,13 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
       // Every problem with offsets has the routed experts' ones.
       for (int pi = 0; pi < p.n_probs; ++pi)
         if (p.pr[pi].offsets)
-          for (int g = lane; g <= p.pr[pi].n_groups; g += 32) table.at[g] = p.pr[pi].offsets[g];
+          for (int g = lane; g <= p.pr[pi].n_groups; g += 32) offsets.at[g] = p.pr[pi].offsets[g];
     } else {
       int run = 0, ne = 0;
       for (int pi = 0; pi < p.n_probs; ++pi)
-        sched_add(table, pi, p.pr[pi].offsets, p.pr[pi].n_groups, p.pr[pi].rows, BMP, (p.pr[pi].N + BN - 1) / BN,
+        sched_add(sched, pi, p.pr[pi].offsets, p.pr[pi].n_groups, p.pr[pi].rows, BMP, (p.pr[pi].N + BN - 1) / BN,
                   p.status, run, ne);
-      sched_close(table, p.n_probs, run, ne);
+      sched_close(sched, p.n_probs, run, ne);
     }
   }
   tc_fence_before();
@@ -605,8 +617,8 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   Tiles<RAGGED_K> tiles;  // the same in both CTAs of the pair
-  if constexpr (RAGGED_K) tiles.init(table.at, p, (int)cluster_id_x(), (int)nclusters_x());
-  else tiles.init(&table, p, (int)cluster_id_x(), (int)nclusters_x());
+  if constexpr (RAGGED_K) tiles.init(offsets.at, p, id, n);
+  else tiles.init(&sched, p, id, n);
   const uint32_t leader_full0 = mapa_shared(full0, 0), leader_tempty0 = mapa_shared(tempty0, 0);
   Tile t;
 
@@ -818,6 +830,20 @@ mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__
   }
 }
 
+template <bool RAGGED_K>
+__global__ void __launch_bounds__(kThreads + (RAGGED_K ? 32 : 0), 1)
+mlp_bwd_pair_kernel(const __grid_constant__ GemmMaps tm, const __grid_constant__ GemmParams p) {
+  pair_gemm<RAGGED_K>(tm, p, (int)cluster_id_x(), (int)nclusters_x());
+}
+
+__global__ void __launch_bounds__(kThreads + 32, 1)
+mlp_bwd_both_kernel(const __grid_constant__ BothMaps tm, const __grid_constant__ BothParams p) {
+  const int id = (int)cluster_id_x(), n = (int)nclusters_x();
+  const int nx = p.x_pairs < n ? p.x_pairs : n - 1;  // a pair for dW at least
+  if (id < nx) pair_gemm<false>(tm.x, p.x, id, nx);
+  else pair_gemm<true>(tm.w, p.w, id - nx, n - nx);
+}
+
 // ------------------------------------------------------------ host side
 typedef CUresult (*TensorMapEncoder)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                      const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
@@ -867,7 +893,7 @@ bool stored_grouped(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols,
   return make_map(m, ptr, cols, rows, z, 64, 32, true);
 }
 
-template <auto kern, int threads, uint32_t staging, typename Maps, typename Params>
+template <auto kern, int threads, uint32_t staging, int min_clusters = 1, typename Maps, typename Params>
 int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cudaStream_t stream) {
   if (max_tiles == 0) return MOE_OK;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(staging)));
@@ -892,7 +918,7 @@ int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cuda
     return n;
   }();
   int clusters = max_clusters;
-  if (clusters < 1) return MOE_ERR_UNSUPPORTED;
+  if (clusters < min_clusters) return MOE_ERR_UNSUPPORTED;
   if (max_tiles < clusters) clusters = (int)max_tiles;
   cfg.gridDim = dim3(2 * (unsigned)clusters);
   MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, maps, params));
@@ -900,8 +926,53 @@ int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cuda
 }
 
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Row tiles at most, whatever the groups' sizes, and as many as groups of
+// about the same size have.
 inline int64_t row_tiles(const MlpBwdProblem &q) { return div_up(q.rows, BMP) + (q.offsets ? q.n_groups : 0); }
+inline int64_t likely_row_tiles(const MlpBwdProblem &q) {
+  if (!q.offsets) return div_up(q.rows, BMP);
+  const int64_t few = q.rows < q.n_groups ? q.rows : q.n_groups, many = div_up(q.rows, BMP) + q.n_groups / 2;
+  return few > many ? few : many;
+}
 constexpr int64_t kMaxTiles = 0x7fffffff;
+
+// dX and dW do not depend on each other. In turn, a dX of few tiles leaves
+// pairs idle, a small group's dX only reads and its dW only writes, and there
+// is a launch more. Side by side in one launch they fill each other's gaps,
+// but the pairs are split once, so a few long tiles may fit worse. The rule
+// predicts both sides' times in K blocks of a tile; a tile's stores take as
+// long as about 6. With groups of up to 384 rows dW is all stores, in many
+// small tiles: always side by side. Otherwise it has to gain a sixteenth.
+// In turn -> side by side: 64 SwiGLU experts 2048 x 1024, 512 tokens 638 -> 606
+// us, 32 tokens 468 -> 465; 32 of 2048 x 768, 1024 tokens 294 -> 273; 19
+// experts 1152 x 3200, 64 tokens 190 -> 173; two experts 64 x 64 30 -> 21.
+// Where it is refused: one expert 512 x 4096, 9000 tokens 208 -> 233. 117
+// sizes, 96 of them random, take 0.87 of the time in the mean; the one worse
+// by more than drift was 64 experts 256 x 8192, 116 tokens, 544 -> 568.
+constexpr int64_t kStoreBlocks = 6;
+struct SideCost {
+  int64_t tiles = 0, blocks = 0;  // blocks: in K blocks of a tile
+  void add(int64_t t, int64_t kb) { tiles += t; blocks += t * (kb < kStoreBlocks ? kStoreBlocks : kb); }
+  int64_t span(int64_t pairs) const { return div_up(tiles, pairs) * blocks / tiles; }
+};
+
+// The pairs that run dX so that both sides end soonest; 0 for one after the other.
+int split_pairs(const SideCost &x_most, const SideCost &x_likely, const SideCost &w) {
+  int64_t n = num_sms() / 2;
+  // One tile more than pairs is a second chain of loads: as many as there can
+  // be if those fit, else as many as there likely are.
+  const SideCost &x = x_most.tiles <= n ? x_most : x_likely;
+  if (x.tiles == 0 || w.tiles == 0) return 0;
+  if (n > x.tiles + w.tiles) n = x.tiles + w.tiles;
+  int64_t best = INT64_MAX;
+  int pairs = 0;
+  for (int64_t k = 1; k < n && k <= x.tiles; ++k) {
+    const int64_t a = x.span(k), b = w.span(n - k), both = a > b ? a : b;
+    if (both < best) { best = both; pairs = (int)k; }
+  }
+  const bool stores = w.blocks == w.tiles * kStoreBlocks;
+  return stores || best * 16 <= (x.span(n) + w.span(n)) * 15 ? pairs : 0;
+}
 
 // Problems i of `q` with rows, in one launch (all gated or none).
 int run_act_grad(const MlpBwdProblem *q, int n, bool gated, int32_t *status, cudaStream_t stream) {
@@ -937,50 +1008,56 @@ int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStre
   int st = run_act_grad(q, n, false, status, stream);
   if (st == MOE_OK) st = run_act_grad(q, n, true, status, stream);
   if (st != MOE_OK) return st;
-  GemmMaps maps;
-  GemmParams pd;
+  BothMaps maps;
+  BothParams pd;
   memset(&maps, 0, sizeof(maps));
   memset(&pd, 0, sizeof(pd));
-  pd.status = status;
-  int64_t tiles = 0;
+  pd.x.status = pd.w.status = status;
+  int64_t x_tiles = 0, w_tiles = 0;
+  SideCost x_most, x_likely, w_side;
   for (int i = 0; i < n; ++i) {  // dX = dU W1
     const MlpBwdProblem &s = q[i];
     if (!s.dx || s.rows == 0) continue;
-    const int k = pd.n_probs++, h1 = s.gated ? 2 * s.h : s.h;
-    GemmProb &o = pd.pr[k];
+    const int k = pd.x.n_probs++, h1 = s.gated ? 2 * s.h : s.h;
+    GemmProb &o = pd.x.pr[k];
     o.offsets = s.offsets; o.n_groups = s.n_groups; o.rows = s.rows; o.N = s.d; o.K = h1;
     o.out = static_cast<__nv_bfloat16 *>(s.dx);
-    if (!operand_k(&maps.a[k], s.dU, s.rows, h1) || !operand_mn(&maps.b[k], s.W1, h1, s.d, s.n_groups))
+    if (!operand_k(&maps.x.a[k], s.dU, s.rows, h1) || !operand_mn(&maps.x.b[k], s.W1, h1, s.d, s.n_groups))
       return MOE_ERR_CUDA;
-    o.tma_out = stored(&maps.o[k], s.dx, s.rows, s.d);
-    tiles += row_tiles(s) * div_up(s.d, BN);
+    o.tma_out = stored(&maps.x.o[k], s.dx, s.rows, s.d);
+    x_tiles += row_tiles(s) * div_up(s.d, BN);
+    x_most.add(row_tiles(s) * div_up(s.d, BN), div_up(h1, BK));
+    x_likely.add(likely_row_tiles(s) * div_up(s.d, BN), div_up(h1, BK));
   }
-  if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
-  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>, kThreads, kStgBytes>(maps, pd, tiles, stream)) != MOE_OK) return st;
-  memset(&maps, 0, sizeof(maps));
-  memset(&pd, 0, sizeof(pd));
-  pd.status = status;
-  tiles = 0;
+  if (x_tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
   for (int i = n - 1; i >= 0; --i)   // the shared expert's long K first
     for (int which = 0; which < 2; ++which) {
       const MlpBwdProblem &s = q[i];
       void *out = which ? s.dW1 : s.dW2;
       if (!out) continue;
-      const int k = pd.n_probs++, h1 = s.gated ? 2 * s.h : s.h;
-      GemmProb &o = pd.pr[k];
+      const int k = pd.w.n_probs++, h1 = s.gated ? 2 * s.h : s.h;
+      GemmProb &o = pd.w.pr[k];
       o.offsets = s.offsets; o.n_groups = s.n_groups; o.rows = s.rows;
       o.M = which ? h1 : s.d;  // dW1 = dU^T X, dW2 = dY^T H
       o.N = which ? s.d : s.h;
       o.out = static_cast<__nv_bfloat16 *>(out);
       const void *A = which ? s.dU : s.dy, *B = which ? s.x : s.H;
-      if (s.rows > 0 && (!operand_mn(&maps.a[k], A, s.rows, o.M, 0) || !operand_mn(&maps.b[k], B, s.rows, o.N, 0)))
+      if (s.rows > 0 && (!operand_mn(&maps.w.a[k], A, s.rows, o.M, 0) || !operand_mn(&maps.w.b[k], B, s.rows, o.N, 0)))
         return MOE_ERR_CUDA;
-      if (!stored_grouped(&maps.o[k], out, o.M, o.N, s.n_groups)) return MOE_ERR_CUDA;
-      tiles += s.n_groups * div_up(o.M, BMP) * div_up(o.N, BN);
-      if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
-      o.tile_end = (int)tiles;
+      if (!stored_grouped(&maps.w.o[k], out, o.M, o.N, s.n_groups)) return MOE_ERR_CUDA;
+      const int64_t tiles = s.n_groups * div_up(o.M, BMP) * div_up(o.N, BN), kb = div_up(s.rows, (int64_t)s.n_groups * BK);
+      w_tiles += tiles;
+      w_side.add(tiles, kb);
+      if (w_tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
+      o.tile_end = (int)w_tiles;
     }
-  return launch_pairs<mlp_bwd_pair_kernel<true>, kThreads + 32, staging_bytes(true)>(maps, pd, tiles, stream);
+  pd.x_pairs = split_pairs(x_most, x_likely, w_side);
+  if (pd.x_pairs > 0)
+    return launch_pairs<mlp_bwd_both_kernel, kThreads + 32, staging_bytes(true), 2>(maps, pd, x_tiles + w_tiles, stream);
+  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>, kThreads, staging_bytes(true)>(maps.x, pd.x, x_tiles, stream)) !=
+      MOE_OK)
+    return st;
+  return launch_pairs<mlp_bwd_pair_kernel<true>, kThreads + 32, staging_bytes(true)>(maps.w, pd.w, w_tiles, stream);
 }
 
 }  // namespace moe

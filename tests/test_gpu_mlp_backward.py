@@ -234,3 +234,23 @@ def test_another_stream_and_a_captured_graph():
         v.zero_()
     graph.replay()
     same(out)
+
+
+@pytest.mark.parametrize("c", [CASES[n] for n in ("gelu_tiles", "swiglu_tiles", "narrow", "no_rows", "many_tails",
+                                                  "tails_and_blocks")] + [
+    dict(d=256, h=264, act="gelu", dtype="bf16", counts=[1000, 303]),  # dW's K is long, dX has more tiles than likely
+    dict(d=256, h=4608, act="gelu", dtype="bf16", counts=[8500, 7500]),  # few long tiles on both sides
+], ids=str)
+def test_dx_and_dw_do_not_depend_on_being_asked_for_together(c):
+    # Which launch a tile runs in changes neither its products nor their order.
+    m = _moe()
+    cfg, off, o, dt = make(c)
+    G, off, mc = {k: v.cuda() for k, v in o.items()}, off.cuda(), m.make_config(cfg)
+    ws, status = m.alloc_backward_workspace(mc), torch.zeros(1, dtype=torch.int32, device="cuda")
+    both, apart = outputs(cfg, o, dt), outputs(cfg, o, dt)
+    call(m, mc, off, G, both, status, ws)
+    for side in ([k for k in apart if k.startswith("dx")], [k for k in apart if k.startswith("dW")]):
+        call(m, mc, off, G, {k: apart[k] for k in side}, status, ws)
+    assert status.item() == 0
+    for k in both:
+        assert torch.equal(both[k].view(torch.int16), apart[k].view(torch.int16)), k
