@@ -22,12 +22,13 @@
 // condition row. A warp per row needs no barriers, but a lane then holds 36
 // and more columns: too few warps fit an SM to hide their latencies
 // (8192 x 1152, LayerNorm: forward 24 us, backward 50-55 us, against 16 and
-// 25 + 4.5 here; copies of as many bytes take 18.5 and 24.4).
+// 25 + 4.5 here; elementwise kernels over as many bytes take 12.9 and 18.4).
 // Variances are sums of squares of centred values (two reductions), not
 // differences of moments: with a mean of 100 standard deviations the latter
 // would lose 4 digits. Everything between the loads and the stores is fp32,
 // most of it on packed pairs.
 #include "backward.h"
+#include "chained.cuh"
 
 namespace moe {
 namespace {
@@ -512,6 +513,7 @@ __global__ void __launch_bounds__(MAXT, bwd_ctas(MAXT)) block_norm_bwd_vec_kerne
   __shared__ __align__(16) float red_buf[2 * kVecWarps * 8];
   extern __shared__ __align__(16) uint8_t ring[];
   VecReducer red{red_buf, 0};
+  chain_next();
   Fetch<T, 4 * R, kBwdDepth> rows{reinterpret_cast<T *>(ring) + threadIdx.x * 8, 0};
   const T *h = static_cast<const T *>(a.h), *y = static_cast<const T *>(a.yin);
   const T *dz = static_cast<const T *>(a.dz), *dy = static_cast<const T *>(a.dy);  // either may be dh or dx
@@ -724,6 +726,7 @@ __global__ void __launch_bounds__(512) block_norm_bwd_kernel(BlockNormArgs a, No
                                                              float *wpart) {
   constexpr int NV = 2, R = 1;
   __shared__ float red_buf[2 * kMaxWarps * 2 * R];
+  chain_next();
   const T *h = static_cast<const T *>(a.h), *y = static_cast<const T *>(a.yin);
   const T *dz = static_cast<const T *>(a.dz), *dy = static_cast<const T *>(a.dy);  // either may be dh or dx
   const T *gate = static_cast<const T *>(a.gate), *scale = static_cast<const T *>(a.scale);
@@ -903,6 +906,8 @@ struct NormSums {
 template <typename T>
 __global__ void __launch_bounds__(32 * kSlices) block_norm_sum_kernel(BlockNormArgs a, NormSums q) {
   __shared__ __align__(16) float sh[3][kSlices][128];
+  chain_wait();
+  chain_next();
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t list = q.first + blockIdx.y;
   const bool cond = list < q.groups;
@@ -1038,12 +1043,12 @@ int run_bwd(const BlockNormArgs &a, cudaStream_t stream) {
   const int64_t end = p.groups + (wpart ? kWeightLists : 0);
   for (q.first = part ? 0 : p.groups; q.first < end; q.first += 65535) {
     const unsigned n = (unsigned)(end - q.first < 65535 ? end - q.first : 65535);
-    block_norm_sum_kernel<T><<<dim3(blocks, n), 32 * kSlices, 0, stream>>>(a, q);
+    launch_chained(block_norm_sum_kernel<T>, dim3(blocks, n), 32 * kSlices, 0, stream, a, q);
   }
   if (wpart) {
     q.first = p.groups;
     q.last = 1;
-    block_norm_sum_kernel<T><<<dim3(blocks, 1), 32 * kSlices, 0, stream>>>(a, q);
+    launch_chained(block_norm_sum_kernel<T>, dim3(blocks, 1), 32 * kSlices, 0, stream, a, q);
   }
   return last_launch_status();
 }

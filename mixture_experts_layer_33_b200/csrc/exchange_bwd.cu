@@ -14,6 +14,7 @@
 // issues the loads of several chunks before any arithmetic. Dot products and
 // sums are fp32 in a fixed order; nothing is accumulated by atomics.
 #include "backward.h"
+#include "chained.cuh"
 
 namespace moe {
 namespace {
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(ExchangeBwdArgs a
   T *__restrict__ out = static_cast<T *>(a.dy_perm);
   const int lane = threadIdx.x & 31;
   const int64_t asg = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  chain_next();
   if (asg < a.n_assign) {
     int s = 0, e = 0;
     const T *src = nullptr;
@@ -227,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, 4) const_grad_kernel(ExchangeBwdArgs
   const int col = (blockIdx.z * kThreads + tid) * 8;
   const bool live = col < a.d;
   const int64_t lo = a.n_assign * blockIdx.x / chunks, hi = a.n_assign * (blockIdx.x + 1) / chunks;
+  chain_wait();
+  chain_next();
   float av[8], aq[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) av[i] = aq[i] = 0.f;
@@ -275,6 +279,7 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices / 4) const_grad_sum_kern
   __shared__ __align__(16) float sh[kSumSlices][kSumCols];
   const int quad = threadIdx.x % (kSumCols / 4), slice = threadIdx.x / (kSumCols / 4);
   const int64_t c0 = (int64_t)blockIdx.x * kSumCols;
+  chain_wait();
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c0 + quad * 4 < n) {
     const int lo = chunks * slice / kSumSlices, hi = chunks * (slice + 1) / kSumSlices;
@@ -510,9 +515,9 @@ int launch_combine_bwd(const ExchangeBwdArgs &args, const KindTable &kinds, cuda
     const dim3 grid(chunks, a.n_const, (a.d + kThreads * 8 - 1) / (kThreads * 8));
     const auto b = a.const_mix ? const_grad_kernel<__nv_bfloat16, true> : const_grad_kernel<__nv_bfloat16, false>;
     const auto f = a.const_mix ? const_grad_kernel<float, true> : const_grad_kernel<float, false>;
-    (bf16 ? b : f)<<<grid, kThreads, 0, stream>>>(a, kinds, chunks);
-    const_grad_sum_kernel<<<(unsigned)((n + kSumCols - 1) / kSumCols), kSumCols * kSumSlices / 4, 0, stream>>>(
-        a.const_part, a.dconst, chunks, n, a.d, a.const_mix);
+    launch_chained(bf16 ? b : f, grid, kThreads, 0, stream, a, kinds, chunks);
+    launch_chained(const_grad_sum_kernel, (unsigned)((n + kSumCols - 1) / kSumCols), kSumCols * kSumSlices / 4, 0,
+                   stream, a.const_part, a.dconst, chunks, n, a.d, a.const_mix);
   }
   return last_launch_status();
 }

@@ -17,10 +17,13 @@
 // bf16 layers multiply on bf16 mma.sync (as the router's forward does: N = E
 // is far too narrow for a tcgen05 tile). dz is fp32 and enters as the sum of
 // three bf16 terms (8 mantissa bits each, 24 in all), so the products keep
-// fp32 accuracy while x and W_r are exact. 8192 x 1152, 19 experts: 6.5 + 18 +
-// 4 us, 28.7 back to back, where a copy of x takes 13; the middle launch keeps
-// the tensor pipe 44 % and L1 65 % busy (three terms, experts padded to 32).
+// fp32 accuracy while x and W_r are exact. 8192 x 1152, 19 experts: 24.7 us, 22.1
+// in a graph, where an elementwise kernel over as many bytes takes 7.7; launched
+// apart 6.4 + 17.8 + 4, the middle one with the tensor pipe 44 % and L1 65 % busy
+// (three terms, experts padded to 32). The terms one after the other along K
+// (4 steps of 16 instead of 6) took 24.6 us in a graph against 23.5 then.
 #include "backward.h"
+#include "chained.cuh"
 #include "mma_sync.cuh"
 
 namespace moe {
@@ -38,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) router_dz_kernel(RouterBwdArgs a) {
   const int lane = threadIdx.x & 31;
   const bool ec = a.routing == MOE_EXPERT_CHOICE;
   const bool renorm = a.renorm && a.routing == MOE_TOKEN_TOPK;
+  chain_next();
   for (int64_t s = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); s < a.T; s += (int64_t)gridDim.x * kWarps) {
     float A[VPL], dA[VPL];
 #pragma unroll
@@ -123,10 +127,30 @@ __device__ __forceinline__ void mma2(float (&c0)[4], float (&c1)[4], const uint3
   mma_bf16_16816(c1, a, {b[2], b[3]});
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// v[n] of lane q becomes v[q] of lane n, among four neighbouring lanes: swaps
+// with the lane 1 away, then with the lane 2 away.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[4], int q) {
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool up = q & b;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (!(n & b)) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[n] : v[n | b], b);
+        if (up) v[n] = got;
+        else v[n | b] = got;
+      }
+  }
+}
+
 // MT: E padded to 16 MT experts. Shared memory, bf16, rows padded by 8 to
 // spread ldmatrix rows over the banks: two x tiles [TT][TC] (the next one
 // is fetched while one is worked on), the W_r columns [16 MT][TC], dz as three
-// terms [3][TT][16 MT]; the dx tile goes out through its x tile's space.
+// terms [3][TT][16 MT].
 template <int MT> struct RbSmem {
   static constexpr int EP = 16 * MT;
   static constexpr int XP = TC + 8, ZP = EP + 8;
@@ -191,6 +215,8 @@ __global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs
   const bool want_b = a.dbias && blockIdx.x == 0;
   float bias_sum = 0.f;
   fetch_x(t_lo);
+  chain_wait();
+  chain_next();
   fetch_z(t_lo);
   for (int t = t_lo; t < t_hi; ++t) {
     const int s0 = t * TT;
@@ -250,20 +276,20 @@ __global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs
           for (int p = 0; p < 3; ++p) mma2(o[n], o[n + 1], f[p], b);
         }
       }
-      __syncthreads();  // the x tile has been read by every warp
+      // A lane holds two columns of every 8: the four lanes of a row trade
+      // them for whole 16-byte pieces, lane q those of block 4 g + q.
+      const int q = lane & 3;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int r = r0 + (lane >> 2), c = cw + n * 8 + (lane & 3) * 2;
-        *reinterpret_cast<__nv_bfloat162 *>(sx + r * XP + c) = __floats2bfloat162_rn(o[n][0], o[n][1]);
-        *reinterpret_cast<__nv_bfloat162 *>(sx + (r + 8) * XP + c) = __floats2bfloat162_rn(o[n][2], o[n][3]);
-      }
-      __syncthreads();
-      for (int i = tid; i < TT * (TC / 8); i += kThreads) {
-        const int r = i / (TC / 8), c = (i % (TC / 8)) * 8;
-        if (s0 + r < a.T && c0 + c < a.d)
-          *reinterpret_cast<uint4 *>(dx + (size_t)(s0 + r) * a.d + c0 + c) =
-              *reinterpret_cast<const uint4 *>(sx + r * XP + c);
-      }
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) v[n] = pack_bf16(o[4 * g + n][2 * half], o[4 * g + n][2 * half + 1]);
+          transpose4(v, q);
+          const int r = s0 + r0 + (lane >> 2) + 8 * half, c = c0 + cw + (4 * g + q) * 8;
+          if (r < a.T && c < a.d) *reinterpret_cast<uint4 *>(dx + (size_t)r * a.d + c) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
     }
   }
   if (want_w) {
@@ -316,6 +342,8 @@ __global__ void __launch_bounds__(kThreads) router_bwd_f32_kernel(RouterBwdArgs 
       *reinterpret_cast<float4 *>(sw + i * 4) =
           c < a.d ? *reinterpret_cast<const float4 *>(wr + (size_t)e * a.d + c) : zero;
     }
+  chain_wait();
+  chain_next();
   const bool want_b = a.dbias && blockIdx.x == 0;
   float bias_sum[16];  // experts warp + 8 i, in lane 0
 #pragma unroll
@@ -398,6 +426,7 @@ __global__ void __launch_bounds__(kSumThreads) router_bwd_sum_kernel(const float
                                                                      float *dW_r, float *dbias, int E, int d,
                                                                      int splits) {
   __shared__ __align__(16) float sh[kSumSlices][kSumCols];
+  chain_wait();
   const int64_t nw = dW_r ? (int64_t)E * d : 0, c0 = (int64_t)blockIdx.x * kSumCols;
   if (c0 >= nw) {  // dbias: a thread per expert and slice of the list
     const int width = E <= 32 ? 32 : E <= 64 ? 64 : 128, slices = kSumThreads / width;
@@ -454,7 +483,7 @@ int run_bf16(const RouterBwdArgs &a, int splits, float *bias_part, cudaStream_t 
   const dim3 grid((a.d + TC - 1) / TC, splits);
   MOE_CUDA_TRY(cudaFuncSetAttribute(router_bwd_bf16_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)RbSmem<MT>::total));
-  router_bwd_bf16_kernel<MT><<<grid, kThreads, RbSmem<MT>::total, stream>>>(a, splits, bias_part);
+  launch_chained(router_bwd_bf16_kernel<MT>, grid, kThreads, RbSmem<MT>::total, stream, a, splits, bias_part);
   return last_launch_status();
 }
 
@@ -488,14 +517,14 @@ int launch_router_bwd(const RouterBwdArgs &a, cudaStream_t stream) {
                         : a.E <= 32 ? router_bwd_f32_kernel<8>
                                     : router_bwd_f32_kernel<32>;
       MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-      kern<<<dim3((a.d + FC - 1) / FC, splits), kThreads, smem, stream>>>(a, splits, bias_part);
+      launch_chained(kern, dim3((a.d + FC - 1) / FC, splits), kThreads, smem, stream, a, splits, bias_part);
       st = last_launch_status();
     }
   }
   if (st != MOE_OK || (!a.dW_r && !a.dbias)) return st;
   const int64_t blocks = (a.dW_r ? ((int64_t)a.E * a.d + kSumCols - 1) / kSumCols : 0) + (a.dbias ? 1 : 0);
-  router_bwd_sum_kernel<<<(unsigned)blocks, kSumThreads, 0, stream>>>(a.part, bias_part, a.dW_r, a.dbias, a.E, a.d,
-                                                                     splits);
+  launch_chained(router_bwd_sum_kernel, (unsigned)blocks, kSumThreads, 0, stream, a.part, bias_part, a.dW_r, a.dbias,
+                 a.E, a.d, splits);
   return last_launch_status();
 }
 
