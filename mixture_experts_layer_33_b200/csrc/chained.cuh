@@ -8,7 +8,8 @@
 // so completion carries over from launch to launch.
 // One call after the other, against ordinary launches: router 8192 x 1152 with
 // 19 experts 28.7 -> 24.7 us, combine with constant experts (4099 x 1152) 28.7
-// -> 24.5, block norm gradient 8192 x 1152 30.8 -> 28.9.
+// -> 24.5, block norm gradient 8192 x 1152 30.8 -> 28.9, MLP gradient of two
+// experts 64 x 64 23.5 -> 21.7 and of DiT-MoE-XL 1657 -> 1643.
 #pragma once
 
 #include "internal.h"

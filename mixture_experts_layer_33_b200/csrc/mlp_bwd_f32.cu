@@ -12,6 +12,7 @@
 // Each K tile's products are summed on their own and then added to the
 // running sum, which shortens the chains of rounding for long K.
 #include "backward.h"
+#include "chained.cuh"
 
 namespace moe {
 namespace {
@@ -54,6 +55,8 @@ __global__ void __launch_bounds__(kThreads) mlp_bwd_gemm_kernel(Gemm p) {
     }
     s_group = g; s_lo = r0; s_hi = r1;
   }
+  chain_next();
+  chain_wait();
   __syncthreads();
   const int g = s_group;
   if (g < 0) return;
@@ -143,31 +146,35 @@ int run(const MlpBwdProblem &p, cudaStream_t stream) {
   Gemm g{};
   g.offsets = p.offsets; g.n_groups = p.n_groups; g.rows = p.rows; g.gated = p.gated; g.status = p.status;
   g.U = static_cast<float *>(p.U); g.H = p.H; g.dU = p.dU;
+  bool chained = false;
+  auto launch = [&](void (*kern)(Gemm), dim3 grid, const Gemm &q) {
+    if (chained) launch_chained(kern, grid, kThreads, 0, stream, q);
+    else kern<<<grid, kThreads, 0, stream>>>(q);
+    chained = true;
+  };
   if (p.rows > 0) {
     Gemm a = g;  // U = X W1^T
     a.A = p.x; a.lda = p.d; a.B = p.W1; a.ldb = p.d; a.b_group = (int64_t)up * p.d; a.N = up; a.K = p.d;
-    mlp_bwd_gemm_kernel<false, true, false, kStoreU><<<dim3(tiles(up), (unsigned)mt), kThreads, 0, stream>>>(a);
+    launch(mlp_bwd_gemm_kernel<false, true, false, kStoreU>, dim3(tiles(up), (unsigned)mt), a);
     Gemm b = g;  // dH = dY W2, then H and dU
     b.A = p.dy; b.lda = p.d; b.B = p.W2; b.ldb = p.h; b.b_group = (int64_t)p.h * p.d; b.N = p.h; b.K = p.d;
-    mlp_bwd_gemm_kernel<false, false, false, kActGrad><<<dim3(tiles(p.h), (unsigned)mt), kThreads, 0, stream>>>(b);
+    launch(mlp_bwd_gemm_kernel<false, false, false, kActGrad>, dim3(tiles(p.h), (unsigned)mt), b);
     if (p.dx) {
       Gemm c = g;  // dX = dU W1
       c.A = p.dU; c.lda = up; c.B = p.W1; c.ldb = p.d; c.b_group = (int64_t)up * p.d; c.N = p.d; c.K = up;
       c.out = p.dx;
-      mlp_bwd_gemm_kernel<false, false, false, kStore><<<dim3(tiles(p.d), (unsigned)mt), kThreads, 0, stream>>>(c);
+      launch(mlp_bwd_gemm_kernel<false, false, false, kStore>, dim3(tiles(p.d), (unsigned)mt), c);
     }
   }
   if (p.dW2) {
     Gemm w = g;  // dW2 = dY^T H
     w.A = p.dy; w.lda = p.d; w.B = p.H; w.ldb = p.h; w.M = p.d; w.N = p.h; w.out = p.dW2;
-    mlp_bwd_gemm_kernel<true, false, true, kStore>
-        <<<dim3(tiles(p.h), tiles(p.d), p.n_groups), kThreads, 0, stream>>>(w);
+    launch(mlp_bwd_gemm_kernel<true, false, true, kStore>, dim3(tiles(p.h), tiles(p.d), p.n_groups), w);
   }
   if (p.dW1) {
     Gemm w = g;  // dW1 = dU^T X
     w.A = p.dU; w.lda = up; w.B = p.x; w.ldb = p.d; w.M = up; w.N = p.d; w.out = p.dW1;
-    mlp_bwd_gemm_kernel<true, false, true, kStore>
-        <<<dim3(tiles(p.d), tiles(up), p.n_groups), kThreads, 0, stream>>>(w);
+    launch(mlp_bwd_gemm_kernel<true, false, true, kStore>, dim3(tiles(p.d), tiles(up), p.n_groups), w);
   }
   return last_launch_status();
 }

@@ -23,7 +23,7 @@
 // DiT-MoE-XL (8 experts that share 16384 rows, two shared experts of 8192
 // each, 1152 x 4608, 1.74 TFLOP): 525-548 + 222-247 + 540-562 us launched
 // apart (1270-1325, 1410-1565 and 1240-1290 TFLOP/s of a 1660 burst peak),
-// 1.64-1.67 ms back to back under the power limit (1393 TFLOP/s sustained
+// 1.63-1.70 ms back to back under the power limit (1393 TFLOP/s sustained
 // peak). 64 SwiGLU experts that share 256 rows, 2048 x 1024: 145-154 + 77-82 +
 // 183-185 us for 805 MB read, 537 MB read and 805 MB written; a plain read of
 // 805 MB takes 147 us, a plain fill 208.
@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "backward.h"
+#include "chained.cuh"
 #include "gemm_sched.cuh"
 #include "tc_ptx.cuh"
 
@@ -234,6 +235,7 @@ act_grad_kernel(const __grid_constant__ ActGradMaps tm, const __grid_constant__ 
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = (int)cluster_id_x(), npairs = (int)nclusters_x();
+  chain_next();
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sA = smem_u32(base), sB = sA + STAGES * A_BYTES, sO = sB + STAGES * B_BYTES;
   const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[STAGES]);
@@ -266,6 +268,7 @@ act_grad_kernel(const __grid_constant__ ActGradMaps tm, const __grid_constant__ 
                 p.status, run, ne);
     sched_close(sched, p.n_probs, run, ne);
   }
+  chain_wait();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer's barriers exist before any cross-CTA arrival
@@ -575,6 +578,7 @@ __device__ __forceinline__ void pair_gemm(const GemmMaps &tm, const GemmParams &
   // stage: the peer may be a ring ahead of the leader, never more.
   const uint32_t peer_tail0 = smem_u32(&bars[3 * STAGES + 5]), leader_peer_tail0 = mapa_shared(peer_tail0, 0);
 
+  chain_next();
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < STAGES; ++s) {
@@ -611,6 +615,10 @@ __device__ __forceinline__ void pair_gemm(const GemmMaps &tm, const GemmParams &
       sched_close(sched, p.n_probs, run, ne);
     }
   }
+  // H and dU are there; some of their rows were written by plain stores, and
+  // the TMA reads them.
+  chain_wait();
+  asm volatile("fence.proxy.async;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer's barriers exist before any cross-CTA arrival
@@ -893,17 +901,20 @@ bool stored_grouped(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols,
   return make_map(m, ptr, cols, rows, z, 64, 32, true);
 }
 
+// `chained`: whether an earlier launch of this call precedes it; true from then on.
 template <auto kern, int threads, uint32_t staging, int min_clusters = 1, typename Maps, typename Params>
-int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cudaStream_t stream) {
+int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cudaStream_t stream, bool &chained) {
   if (max_tiles == 0) return MOE_OK;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(staging)));
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(threads);
@@ -921,6 +932,8 @@ int launch_pairs(const Maps &maps, const Params &params, int64_t max_tiles, cuda
   if (clusters < min_clusters) return MOE_ERR_UNSUPPORTED;
   if (max_tiles < clusters) clusters = (int)max_tiles;
   cfg.gridDim = dim3(2 * (unsigned)clusters);
+  if (chained) cfg.numAttrs = 2;
+  chained = true;
   MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, maps, params));
   return last_launch_status();
 }
@@ -975,7 +988,7 @@ int split_pairs(const SideCost &x_most, const SideCost &x_likely, const SideCost
 }
 
 // Problems i of `q` with rows, in one launch (all gated or none).
-int run_act_grad(const MlpBwdProblem *q, int n, bool gated, int32_t *status, cudaStream_t stream) {
+int run_act_grad(const MlpBwdProblem *q, int n, bool gated, int32_t *status, cudaStream_t stream, bool &chained) {
   ActGradMaps maps;
   ActGradParams pd;
   memset(&maps, 0, sizeof(maps));
@@ -998,15 +1011,16 @@ int run_act_grad(const MlpBwdProblem *q, int n, bool gated, int32_t *status, cud
     tiles += row_tiles(s) * div_up(s.h, gated ? BN / 2 : BN);
   }
   if (tiles > kMaxTiles) return MOE_ERR_UNSUPPORTED;
-  return gated ? launch_pairs<act_grad_kernel<true>, kThreads, kStgBytes>(maps, pd, tiles, stream)
-               : launch_pairs<act_grad_kernel<false>, kThreads, kStgBytes>(maps, pd, tiles, stream);
+  return gated ? launch_pairs<act_grad_kernel<true>, kThreads, kStgBytes>(maps, pd, tiles, stream, chained)
+               : launch_pairs<act_grad_kernel<false>, kThreads, kStgBytes>(maps, pd, tiles, stream, chained);
 }
 
 }  // namespace
 
 int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStream_t stream) {
-  int st = run_act_grad(q, n, false, status, stream);
-  if (st == MOE_OK) st = run_act_grad(q, n, true, status, stream);
+  bool chained = false;
+  int st = run_act_grad(q, n, false, status, stream, chained);
+  if (st == MOE_OK) st = run_act_grad(q, n, true, status, stream, chained);
   if (st != MOE_OK) return st;
   BothMaps maps;
   BothParams pd;
@@ -1053,11 +1067,13 @@ int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStre
     }
   pd.x_pairs = split_pairs(x_most, x_likely, w_side);
   if (pd.x_pairs > 0)
-    return launch_pairs<mlp_bwd_both_kernel, kThreads + 32, staging_bytes(true), 2>(maps, pd, x_tiles + w_tiles, stream);
-  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>, kThreads, staging_bytes(true)>(maps.x, pd.x, x_tiles, stream)) !=
-      MOE_OK)
+    return launch_pairs<mlp_bwd_both_kernel, kThreads + 32, staging_bytes(true), 2>(maps, pd, x_tiles + w_tiles, stream,
+                                                                                  chained);
+  if ((st = launch_pairs<mlp_bwd_pair_kernel<false>, kThreads, staging_bytes(true)>(maps.x, pd.x, x_tiles, stream,
+                                                                                      chained)) != MOE_OK)
     return st;
-  return launch_pairs<mlp_bwd_pair_kernel<true>, kThreads + 32, staging_bytes(true)>(maps.w, pd.w, w_tiles, stream);
+  return launch_pairs<mlp_bwd_pair_kernel<true>, kThreads + 32, staging_bytes(true)>(maps.w, pd.w, w_tiles, stream,
+                                                                                     chained);
 }
 
 }  // namespace moe
