@@ -222,3 +222,64 @@ def test_step_is_repeatable_and_captured():
     torch.cuda.synchronize()
     for k in first:
         assert torch.equal(first[k], held[k]), k
+
+
+def test_two_layers_at_once_with_inputs_changing_between_steps():
+    """Steps of two layers on two streams, eager and as graphs replayed at once. Each step's
+    input is written by the stream itself just before it, nothing waits in between: the bits
+    are those of the same steps one at a time."""
+    layers = [setup(n) for n in ("mmoe", "constmix")]
+    xs, dys, want = [], [], []
+    for m, cfg, inp, layer in layers:
+        g = torch.Generator(device="cuda").manual_seed(7)
+        like = inp["x"]
+        xs.append([torch.randn(like.shape, generator=g, device="cuda").to(like.dtype) for _ in range(3)])
+        dys.append([torch.randn(like.shape, generator=g, device="cuda").to(like.dtype) for _ in range(3)])
+    x_in = [torch.empty_like(x[0]) for x in xs]
+    dy_in = [torch.empty_like(d[0]) for d in dys]
+
+    def step(i):
+        _, _, inp, layer = layers[i]
+        y, s = layer.forward_train(x_in[i], z_prev=inp["z_prev"])
+        return {"y": y, **layer.backward(s, dy_in[i])}
+
+    for i in range(2):
+        want.append([])
+        for k in range(3):
+            x_in[i].copy_(xs[i][k])
+            dy_in[i].copy_(dys[i][k])
+            torch.cuda.synchronize()
+            want[i].append({n: t.clone() for n, t in step(i).items()})
+            torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for r in range(12):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                x_in[i].copy_(xs[i][r % 3])
+                dy_in[i].copy_(dys[i][r % 3])
+                got[i].append(step(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r, out in enumerate(got[i]):
+            for n, t in out.items():
+                assert torch.equal(t, want[i][r % 3][n]), ("eager", i, r, n)
+    graphs, held = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            held.append(step(i))
+    kept = [[], []]
+    for r in range(12):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                x_in[i].copy_(xs[i][r % 3])
+                dy_in[i].copy_(dys[i][r % 3])
+                graphs[i].replay()
+                kept[i].append({n: t.clone() for n, t in held[i].items()})
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r, out in enumerate(kept[i]):
+            for n, t in out.items():
+                assert torch.equal(t, want[i][r % 3][n]), ("graph", i, r, n)
