@@ -545,6 +545,37 @@ def block_norm_backward(n: MoeNormConfig, h, y, dz, dy, ws, dh=None, dx=None, po
         dscp, dshp, dstride, _grad_ptr(ws, "ws", torch.uint8, ws.numel(), dev), ws.numel(), _raw_stream(stream, dev)), "moe_block_norm_backward")
 
 
+def _tensors(*trees):
+    """The device tensors in nested tuples and dicts."""
+    for t in trees:
+        if isinstance(t, torch.Tensor):
+            if t.is_cuda:
+                yield t
+        elif isinstance(t, (tuple, list)):
+            yield from _tensors(*t)
+        elif isinstance(t, dict):
+            yield from _tensors(*t.values())
+
+
+def _run_on(stream, step, inputs):
+    """``step()`` on ``stream`` (None: the current stream, as it is). What the step allocates
+    belongs to ``stream``, so a block it frees goes to later work of that stream only, while its
+    kernels may still be queued; ``inputs`` and the results, which the caller holds and frees, are
+    marked as used by both streams."""
+    if stream is None:
+        return step()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    caller = torch.cuda.current_stream()
+    for t in _tensors(inputs):
+        t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        out = step()
+    for t in _tensors(out):
+        t.record_stream(caller)
+    return out
+
+
 class MoELayer:
     """A configured layer: weights and a workspace resident on one device.
 
@@ -552,6 +583,10 @@ class MoELayer:
     ``layer.forward_train(x)`` runs the same layer step by step and keeps what
     ``layer.backward`` needs to turn dy into the gradients of x, the weights
     and the gate residual.
+
+    All three take a ``stream``: the work runs there, after what that stream
+    already holds, and the results are ready in its order. A layer's calls
+    share its workspaces, so they must not overlap on the device.
     """
 
     def __init__(self, cfg, weights, device="cuda"):
@@ -563,18 +598,26 @@ class MoELayer:
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
     def __call__(self, x, z_prev=None, residual="x", aux=None, stream=None):
+        return _run_on(stream, lambda: self._forward(x, z_prev, residual, aux),
+                       (x, z_prev, residual, aux, self.ws, self.status))
+
+    def _forward(self, x, z_prev, residual, aux):
         y = torch.empty_like(x)
-        res = x if residual == "x" else residual
+        res = x if isinstance(residual, str) else residual
         w = self.w
         forward(self.c, x, w["W_r"], w["W1"], w["W2"], y, self.ws, residual=res, z_prev=z_prev,
                 bias=w.get("logit_bias"), Ws1=w.get("Ws1"), Ws2=w.get("Ws2"),
-                const_vecs=w.get("const_vecs"), aux=aux, dev_status=self.status, stream=stream)
+                const_vecs=w.get("const_vecs"), aux=aux, dev_status=self.status)
         return y
 
     def forward_train(self, x, z_prev=None, residual="x", stream=None):
         """The layer through its stage entry points: (y, saved), ``saved`` holding the routing,
         the dispatched rows and the expert outputs for ``backward``. ``residual`` is "x" (the
         layer adds x), None, or another [T, d] tensor."""
+        return _run_on(stream, lambda: self._forward_train(x, z_prev, residual),
+                       (x, z_prev, residual, self.ws, self.status))
+
+    def _forward_train(self, x, z_prev, residual):
         c, w, dev, i32 = self.c, self.w, x.device, torch.int32
         n, T, E = num_assignments(c), c.T, c.E
         ec = c.routing == EXPERT_CHOICE
@@ -592,34 +635,37 @@ class MoELayer:
         topk = c.routing == TOKEN_TOPK
         router(x, w["W_r"], s["logits"], s["probs"], bias=w.get("logit_bias"), z_prev=z_prev,
                z_prev_scale=c.gate_residual_scale, k=c.k if topk else 0, renorm=c.renorm if topk else 0,
-               idx=s["sel"] if topk else None, w=s["w"] if topk else None, stream=stream)
+               idx=s["sel"] if topk else None, w=s["w"] if topk else None)
         if ec:
-            select_expert_choice(s["probs"], c.group_size, c.capacity, s["sel"], s["w"], stream=stream)
+            select_expert_choice(s["probs"], c.group_size, c.capacity, s["sel"], s["w"])
         elif c.routing == DES_VOTE:
             votes = torch.empty(E, dtype=torch.int64, device=dev)
-            core_set_vote(s["probs"], c.k, c.M_core, votes, ints(c.M_core), s["sel"], s["w"],
-                          stream=stream)
+            core_set_vote(s["probs"], c.k, c.M_core, votes, ints(c.M_core), s["sel"], s["w"])
         elif c.routing == DES_SEQ:
-            core_set_union(s["probs"], c.k, c.k_local, ints(E), ints(1), s["sel"], s["w"], stream=stream)
+            core_set_union(s["probs"], c.k, c.k_local, ints(E), ints(1), s["sel"], s["w"])
         dispatch(c, s["sel"], x, s["x_perm"], s["offsets"], ints(n), s["row_of"], s["tok_ptr"],
-                 s["tok_assign"], self.status, self.ws, stream=stream)
+                 s["tok_assign"], self.status, self.ws)
         y_shared = torch.empty_like(x) if c.n_shared else None
         grouped_mlp(c, s["x_perm"], s["offsets"], w["W1"], w["W2"], x, w.get("Ws1"), w.get("Ws2"),
-                    s["y_perm"], y_shared, self.status, self.ws, stream=stream)
+                    s["y_perm"], y_shared, self.status, self.ws)
         y = torch.empty_like(x)
         combine(c, s["y_perm"], y_shared, s["sel"], s["w"], s["row_of"], s["tok_ptr"],
                 s["tok_assign"], x, w.get("const_vecs"), x if isinstance(residual, str) else residual,
-                y, self.status, stream=stream)
+                y, self.status)
         return y, s
 
     def backward(self, saved, dy, dprobs=None, stream=None):
         """Gradients from dy, the gradient of ``forward_train``'s y (and ``dprobs``, a gradient
         that reaches the affinities directly): a dict of x, W_r, logit_bias, W1, W2, Ws1, Ws2,
         const_vecs and z_prev (those the layer has). A residual other than x has gradient dy."""
+        if self.bws is None:
+            self.bws = _run_on(stream, lambda: alloc_backward_workspace(self.c, dy.device), ())
+        return _run_on(stream, lambda: self._backward(saved, dy, dprobs),
+                       (saved, dy, dprobs, self.bws, self.status))
+
+    def _backward(self, saved, dy, dprobs):
         c, w, s, dev = self.c, self.w, saved, dy.device
         n, x = num_assignments(c), saved["x"]
-        if self.bws is None:
-            self.bws = alloc_backward_workspace(c, dev)
         cv = w.get("const_vecs")
         routing = (s["sel"], s["w"], s["row_of"], s["tok_ptr"], s["tok_assign"], x, cv)
         dy_perm, dw = torch.empty_like(s["y_perm"]), torch.empty(n, device=dev)
@@ -634,20 +680,18 @@ class MoELayer:
         if c.n_shared:
             g["Ws1"], g["Ws2"] = torch.empty_like(w["Ws1"]), torch.empty_like(w["Ws2"])
         combine_backward(c, dy, s["y_perm"], *routing, dy_perm, dw, self.status, self.bws,
-                         dconst=g.get("const_vecs"), stream=stream)
+                         dconst=g.get("const_vecs"))
         dx_perm = torch.empty_like(s["x_perm"])
         dx_shared = torch.empty_like(x) if c.n_shared else None
         grouped_mlp_backward(c, s["x_perm"], s["offsets"], w["W1"], w["W2"], dy_perm, x, w.get("Ws1"),
                              w.get("Ws2"), dy, self.status, self.bws, dx_perm=dx_perm, dW1=g["W1"],
-                             dW2=g["W2"], dx_shared=dx_shared, dWs1=g.get("Ws1"), dWs2=g.get("Ws2"),
-                             stream=stream)
+                             dW2=g["W2"], dx_shared=dx_shared, dWs1=g.get("Ws1"), dWs2=g.get("Ws2"))
         dx_router = torch.empty_like(x)
         router_backward(c, x, w["W_r"], s["probs"], s["sel"], s["w"], dw, s["tok_ptr"], s["tok_assign"],
                         torch.empty_like(s["probs"]), self.status, self.bws, dprobs=dprobs,
-                        dz_prev=g.get("z_prev"), dbias=g.get("logit_bias"), dW_r=g["W_r"], dx=dx_router,
-                        stream=stream)
+                        dz_prev=g.get("z_prev"), dbias=g.get("logit_bias"), dW_r=g["W_r"], dx=dx_router)
         add = [dx_router] + ([dx_shared] if c.n_shared else [])
         if isinstance(s["residual"], str):
             add.append(dy)
-        dispatch_backward(c, dx_perm, dy, *routing, g["x"], self.status, add=add, stream=stream)
+        dispatch_backward(c, dx_perm, dy, *routing, g["x"], self.status, add=add)
         return g
