@@ -512,7 +512,9 @@ MOE_API int moe_combine_backward(const moe_config *cfg, const void *dy, const vo
  *   dy, x    [T, d]; dy is needed with identity or mixed constant experts,
  *            x and const_vecs with mixed constant experts, else nullable
  *   add0..2  [T, d] (dtype), nullable; dx may be the same buffer as any of
- *            them
+ *            them (one of them may be dy: then too, but with mixed constant
+ *            experts, which need whole rows of dy and x, a dx that overlaps
+ *            dy or x is refused)
  *   tok_ptr, tok_assign  expert choice: the token lists of moe_dispatch
  */
 MOE_API int moe_dispatch_backward(const moe_config *cfg, const void *dx_perm, const void *dy,

@@ -15,6 +15,12 @@ bool all_aligned16(P... p) {
   return (aligned16(p) && ...);
 }
 
+// Whether two buffers of `bytes` bytes share any.
+inline bool overlap(const void *a, const void *b, size_t bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return (p < q ? q - p : p - q) < bytes;
+}
+
 // One workspace for the four backward entry points, which run one after
 // another: each takes it from the start.
 struct BwdLayout {
@@ -128,6 +134,9 @@ int moe_dispatch_backward(const moe_config *cfg, const void *dx_perm, const void
     if (c.n_heavy > 0 && !dx_perm) return MOE_ERR_INVALID_ARG;
     if ((has_kind(c, MOE_IDENTITY) || mix) && !dy) return MOE_ERR_INVALID_ARG;
     if (mix && (!x || !const_vecs)) return MOE_ERR_INVALID_ARG;
+    // A mixed constant expert's dots take whole rows of dy and x, of which each warp stores a part.
+    const size_t row_bytes = (size_t)c.d * (c.dtype == MOE_BF16 ? 2 : 4);
+    if (mix && (overlap(dx, dy, c.T * row_bytes) || overlap(dx, x, c.T * row_bytes))) return MOE_ERR_INVALID_ARG;
     if (c.routing == MOE_EXPERT_CHOICE && (!tok_ptr || !tok_assign)) return MOE_ERR_INVALID_ARG;
   }
   if (!all_aligned16(dx_perm, dy, x, const_vecs, add0, add1, add2, dx)) return MOE_ERR_INVALID_ARG;
