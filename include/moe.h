@@ -530,6 +530,7 @@ MOE_API int moe_dispatch_backward(const moe_config *cfg, const void *dx_perm, co
  * renorm under token choice, A / S with S their sum) gives
  *   dA     = dprobs + the dw of each (s, e); renorm: (dw_a - sum_b dw_b w_b) / S
  *   dz     = A (dA - <A, dA>)          z = x W_r^T + bias + scale z_prev
+ *            (z that a further layer takes as z_prev: moe_router_backward_logits)
  *   dx     = dz W_r,  dW_r = dz^T x,  dbias = sum_s dz,  dz_prev = scale dz
  *   probs    [T, E] fp32 (A)           sel, w, tok_ptr, tok_assign: the
  *            selection and (expert choice) its token lists
@@ -549,6 +550,23 @@ MOE_API int moe_router_backward(const moe_config *cfg, const void *x, const void
                         const float *dprobs, float *dlogits, float *dz_prev, float *dbias,
                         float *dW_r, void *dx, int32_t *dev_status, void *ws,
                         size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_router_backward with a gradient on the logits besides the selection's,
+ * as of a layer whose logits the next one takes as z_prev:
+ *   dz = A (dA - <A, dA>) + dz_next
+ *   dz_next  [T, E] fp32, nullable: a gradient that reaches the logits
+ *            directly, the dz_prev of the next layer's call. It may be the
+ *            same buffer as dlogits or dz_prev.
+ * Everything else as there; with dz_next NULL the two calls are the same.
+ */
+MOE_API int moe_router_backward_logits(const moe_config *cfg, const void *x, const void *W_r,
+                                const float *probs, const int32_t *sel, const float *w,
+                                const float *dw, const int32_t *tok_ptr,
+                                const int32_t *tok_assign, const float *dprobs,
+                                const float *dz_next, float *dlogits, float *dz_prev,
+                                float *dbias, float *dW_r, void *dx, int32_t *dev_status,
+                                void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * Gradient of moe_grouped_mlp. The hidden activations are formed again from

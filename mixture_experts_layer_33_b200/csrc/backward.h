@@ -49,7 +49,7 @@ struct RouterBwdArgs {
   int64_t n_assign;
   float zscale;
   const void *x, *W_r;
-  const float *probs, *w, *dw, *dprobs;
+  const float *probs, *w, *dw, *dprobs, *dz_next;
   const int32_t *sel, *tok_ptr, *tok_assign;
   float *dlogits, *dz_prev, *dbias, *dW_r;
   void *dx;

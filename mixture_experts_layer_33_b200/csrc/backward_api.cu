@@ -149,6 +149,15 @@ int moe_router_backward(const moe_config *cfg, const void *x, const void *W_r, c
                         const float *w, const float *dw, const int32_t *tok_ptr, const int32_t *tok_assign,
                         const float *dprobs, float *dlogits, float *dz_prev, float *dbias, float *dW_r, void *dx,
                         int32_t *dev_status, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  return moe_router_backward_logits(cfg, x, W_r, probs, sel, w, dw, tok_ptr, tok_assign, dprobs, nullptr, dlogits,
+                                     dz_prev, dbias, dW_r, dx, dev_status, ws, ws_bytes, stream);
+}
+
+int moe_router_backward_logits(const moe_config *cfg, const void *x, const void *W_r, const float *probs,
+                                const int32_t *sel, const float *w, const float *dw, const int32_t *tok_ptr,
+                                const int32_t *tok_assign, const float *dprobs, const float *dz_next, float *dlogits,
+                                float *dz_prev, float *dbias, float *dW_r, void *dx, int32_t *dev_status, void *ws,
+                                size_t ws_bytes, moe_stream_t stream) {
   int st = check_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config &c = *cfg;
@@ -164,7 +173,7 @@ int moe_router_backward(const moe_config *cfg, const void *x, const void *W_r, c
   RouterBwdArgs a{};
   a.routing = c.routing; a.T = c.T; a.d = c.d; a.E = c.E; a.k = c.k; a.C = c.capacity; a.dtype = c.dtype;
   a.renorm = c.renorm; a.n_assign = n_assign_of(c); a.zscale = c.gate_residual_scale;
-  a.x = x; a.W_r = W_r; a.probs = probs; a.w = w; a.dw = dw; a.dprobs = dprobs;
+  a.x = x; a.W_r = W_r; a.probs = probs; a.w = w; a.dw = dw; a.dprobs = dprobs; a.dz_next = dz_next;
   a.sel = sel; a.tok_ptr = tok_ptr; a.tok_assign = tok_assign;
   a.dlogits = dlogits; a.dz_prev = dz_prev; a.dbias = dbias; a.dW_r = dW_r; a.dx = c.T > 0 ? dx : nullptr;
   a.part = at<float>(ws, kAlign);

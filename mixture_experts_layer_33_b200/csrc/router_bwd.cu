@@ -4,8 +4,9 @@
 // EC-DiT: Scaling Diffusion Transformers with Adaptive Expert-Choice
 // Routing, section 3: A = softmax(x W_r); a selected expert is weighted by
 // its affinity A[s, e]. MMOE, "gate-residual routing": the logits take the
-// previous layer's as a scaled term.
-//   dA = dprobs + scatter(dw),  dz = A (dA - <A, dA>)
+// previous layer's as a scaled term, so the next layer's gradient of that
+// term (dz_next) reaches these logits beside the softmax.
+//   dA = dprobs + scatter(dw),  dz = A (dA - <A, dA>) + dz_next
 //   dx = dz W_r,  dW_r = dz^T x,  dbias = sum_s dz,  dz_prev = scale dz
 //
 // Two products with one narrow side (E <= 128) each: bound by reading x and
@@ -43,12 +44,13 @@ __global__ void __launch_bounds__(kThreads) router_dz_kernel(RouterBwdArgs a) {
   const bool renorm = a.renorm && a.routing == MOE_TOKEN_TOPK;
   chain_next();
   for (int64_t s = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); s < a.T; s += (int64_t)gridDim.x * kWarps) {
-    float A[VPL], dA[VPL];
+    float A[VPL], dA[VPL], zn[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int e = lane + 32 * v;
       A[v] = e < a.E ? a.probs[s * a.E + e] : 0.f;
       dA[v] = (e < a.E && a.dprobs) ? a.dprobs[s * a.E + e] : 0.f;
+      zn[v] = (e < a.E && a.dz_next) ? a.dz_next[s * a.E + e] : 0.f;
     }
     int64_t j0, j1;
     if (ec) {
@@ -109,7 +111,8 @@ __global__ void __launch_bounds__(kThreads) router_dz_kernel(RouterBwdArgs a) {
     for (int v = 0; v < VPL; ++v) {
       const int e = lane + 32 * v;
       if (e >= a.E) continue;
-      const float dz = A[v] * (dA[v] - dot);
+      float dz = A[v] * (dA[v] - dot);
+      if (a.dz_next) dz += zn[v];
       a.dlogits[s * a.E + e] = dz;
       if (a.dz_prev) a.dz_prev[s * a.E + e] = a.zscale * dz;
     }

@@ -39,7 +39,7 @@ ENTRY_POINTS = (
     "moe_grouped_mlp", "moe_combine", "moe_forward", "moe_forward_host",
     "moe_dispatch_noalloc", "moe_activation", "moe_test_set_barrier_wait", "moe_build_flags",
     "moe_backward_workspace_size", "moe_combine_backward", "moe_dispatch_backward",
-    "moe_router_backward", "moe_grouped_mlp_backward", "moe_block_norm",
+    "moe_router_backward", "moe_router_backward_logits", "moe_grouped_mlp_backward", "moe_block_norm",
     "moe_block_norm_workspace_size", "moe_block_norm_backward",
 )
 NOALLOC_SCRATCH_BYTES = 256 * 1024  # MOE_NOALLOC_SCRATCH_BYTES
@@ -99,6 +99,7 @@ _SIGS = {
     "moe_combine_backward": (_i32, [_CFG] + [_vp] * 11 + [_vp, _sz, _vp]),
     "moe_dispatch_backward": (_i32, [_CFG] + [_vp] * 13 + [_vp, _vp]),
     "moe_router_backward": (_i32, [_CFG] + [_vp] * 15 + [_vp, _sz, _vp]),
+    "moe_router_backward_logits": (_i32, [_CFG] + [_vp] * 16 + [_vp, _sz, _vp]),
     "moe_grouped_mlp_backward": (_i32, [_CFG] + [_vp] * 16 + [_vp, _sz, _vp]),
     "moe_block_norm": (_i32, [_NCFG] + [_vp] * 8 + [_i64, _vp, _vp, _vp]),
     "moe_block_norm_workspace_size": (_i32, [_NCFG, ctypes.POINTER(_sz)]),
@@ -430,17 +431,19 @@ def dispatch_backward(c: MoeConfig, dx_perm, dy, sel, w, row_of, tok_ptr, tok_as
 
 def router_backward(c: MoeConfig, x, W_r, probs, sel, w, dw, tok_ptr, tok_assign, dlogits,
                     dev_status, ws, dprobs=None, dz_prev=None, dbias=None, dW_r=None, dx=None,
-                    stream=None):
+                    stream=None, dz_next=None):
     """Gradient of the routing weights back through selection and softmax to the logits, and
-    from there to the router's inputs (moe_router_backward)."""
+    from there to the router's inputs (moe_router_backward). ``dz_next``: the next layer's
+    ``dz_prev``, when it takes these logits as its gate residual (moe_router_backward_logits)."""
     n, dt, f32, i32 = _assignments(c), _layer_dtype(c), torch.float32, torch.int32
     dev = torch.cuda.current_device()
     te = c.T * c.E
-    _check(LIB.moe_router_backward(
+    _check(LIB.moe_router_backward_logits(
         ctypes.byref(c), _grad_ptr(x, "x", dt, c.T * c.d, dev), _grad_ptr(W_r, "W_r", dt, c.E * c.d, dev),
         _grad_ptr(probs, "probs", f32, te, dev), _grad_ptr(sel, "sel", i32, n, dev), _grad_ptr(w, "w", f32, n, dev),
         _grad_ptr(dw, "dw", f32, n, dev), _grad_ptr(tok_ptr, "tok_ptr", i32, c.T + 1, dev),
         _grad_ptr(tok_assign, "tok_assign", i32, n, dev), _grad_ptr(dprobs, "dprobs", f32, te, dev),
+        _grad_ptr(dz_next, "dz_next", f32, te, dev),
         _grad_ptr(dlogits, "dlogits", f32, te, dev), _grad_ptr(dz_prev, "dz_prev", f32, te, dev),
         _grad_ptr(dbias, "dbias", f32, c.E, dev), _grad_ptr(dW_r, "dW_r", f32, c.E * c.d, dev),
         _grad_ptr(dx, "dx", dt, c.T * c.d, dev), _grad_ptr(dev_status, "dev_status", i32, 1, dev),
@@ -654,16 +657,17 @@ class MoELayer:
                 y, self.status)
         return y, s
 
-    def backward(self, saved, dy, dprobs=None, stream=None):
-        """Gradients from dy, the gradient of ``forward_train``'s y (and ``dprobs``, a gradient
-        that reaches the affinities directly): a dict of x, W_r, logit_bias, W1, W2, Ws1, Ws2,
-        const_vecs and z_prev (those the layer has). A residual other than x has gradient dy."""
+    def backward(self, saved, dy, dprobs=None, stream=None, dlogits=None):
+        """Gradients from dy, the gradient of ``forward_train``'s y, and from gradients that reach
+        the affinities (``dprobs``) or the logits (``dlogits``: the z_prev gradient of a next layer
+        whose gate residual is ``saved["logits"]``) directly: a dict of x, W_r, logit_bias, W1, W2,
+        Ws1, Ws2, const_vecs and z_prev (those the layer has). A residual other than x has gradient dy."""
         if self.bws is None:
             self.bws = _run_on(stream, lambda: alloc_backward_workspace(self.c, dy.device), ())
-        return _run_on(stream, lambda: self._backward(saved, dy, dprobs),
-                       (saved, dy, dprobs, self.bws, self.status))
+        return _run_on(stream, lambda: self._backward(saved, dy, dprobs, dlogits),
+                       (saved, dy, dprobs, dlogits, self.bws, self.status))
 
-    def _backward(self, saved, dy, dprobs):
+    def _backward(self, saved, dy, dprobs, dlogits):
         c, w, s, dev = self.c, self.w, saved, dy.device
         n, x = num_assignments(c), saved["x"]
         cv = w.get("const_vecs")
@@ -689,7 +693,8 @@ class MoELayer:
         dx_router = torch.empty_like(x)
         router_backward(c, x, w["W_r"], s["probs"], s["sel"], s["w"], dw, s["tok_ptr"], s["tok_assign"],
                         torch.empty_like(s["probs"]), self.status, self.bws, dprobs=dprobs,
-                        dz_prev=g.get("z_prev"), dbias=g.get("logit_bias"), dW_r=g["W_r"], dx=dx_router)
+                        dz_prev=g.get("z_prev"), dbias=g.get("logit_bias"), dW_r=g["W_r"], dx=dx_router,
+                        dz_next=dlogits)
         add = [dx_router] + ([dx_shared] if c.n_shared else [])
         if isinstance(s["residual"], str):
             add.append(dy)
