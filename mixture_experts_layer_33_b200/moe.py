@@ -608,7 +608,7 @@ class MoELayer:
         y = torch.empty_like(x)
         res = x if isinstance(residual, str) else residual
         w = self.w
-        forward(self.c, x, w["W_r"], w["W1"], w["W2"], y, self.ws, residual=res, z_prev=z_prev,
+        forward(self.c, x, w["W_r"], w.get("W1"), w.get("W2"), y, self.ws, residual=res, z_prev=z_prev,
                 bias=w.get("logit_bias"), Ws1=w.get("Ws1"), Ws2=w.get("Ws2"),
                 const_vecs=w.get("const_vecs"), aux=aux, dev_status=self.status)
         return y
@@ -649,7 +649,7 @@ class MoELayer:
         dispatch(c, s["sel"], x, s["x_perm"], s["offsets"], ints(n), s["row_of"], s["tok_ptr"],
                  s["tok_assign"], self.status, self.ws)
         y_shared = torch.empty_like(x) if c.n_shared else None
-        grouped_mlp(c, s["x_perm"], s["offsets"], w["W1"], w["W2"], x, w.get("Ws1"), w.get("Ws2"),
+        grouped_mlp(c, s["x_perm"], s["offsets"], w.get("W1"), w.get("W2"), x, w.get("Ws1"), w.get("Ws2"),
                     s["y_perm"], y_shared, self.status, self.ws)
         y = torch.empty_like(x)
         combine(c, s["y_perm"], y_shared, s["sel"], s["w"], s["row_of"], s["tok_ptr"],
@@ -661,7 +661,8 @@ class MoELayer:
         """Gradients from dy, the gradient of ``forward_train``'s y, and from gradients that reach
         the affinities (``dprobs``) or the logits (``dlogits``: the z_prev gradient of a next layer
         whose gate residual is ``saved["logits"]``) directly: a dict of x, W_r, logit_bias, W1, W2,
-        Ws1, Ws2, const_vecs and z_prev (those the layer has). A residual other than x has gradient dy."""
+        Ws1, Ws2, const_vecs and z_prev (those the layer has; zero for a weight that none of its experts
+        reads). A residual other than x has gradient dy."""
         if self.bws is None:
             self.bws = _run_on(stream, lambda: alloc_backward_workspace(self.c, dy.device), ())
         return _run_on(stream, lambda: self._backward(saved, dy, dprobs, dlogits),
@@ -670,26 +671,30 @@ class MoELayer:
     def _backward(self, saved, dy, dprobs, dlogits):
         c, w, s, dev = self.c, self.w, saved, dy.device
         n, x = num_assignments(c), saved["x"]
-        cv = w.get("const_vecs")
+        # Weights that none of the layer's experts reads have gradient zero and go no further.
+        used = {"W1": c.n_heavy > 0, "W2": c.n_heavy > 0, "Ws1": c.n_shared > 0, "Ws2": c.n_shared > 0,
+                "const_vecs": _n_const(c) > 0}
+        W = {k: w.get(k) if on else None for k, on in used.items()}
+        cv = W["const_vecs"]
         routing = (s["sel"], s["w"], s["row_of"], s["tok_ptr"], s["tok_assign"], x, cv)
         dy_perm, dw = torch.empty_like(s["y_perm"]), torch.empty(n, device=dev)
-        g = {"W_r": torch.empty(c.E, c.d, device=dev), "W1": torch.empty_like(w["W1"]),
-             "W2": torch.empty_like(w["W2"]), "x": torch.empty_like(x)}
+        g = {"W_r": torch.empty(c.E, c.d, device=dev), "x": torch.empty_like(x)}
+        for k, on in used.items():
+            if w.get(k) is not None:
+                new = torch.empty_like if on else torch.zeros_like
+                g[k] = new(w[k], dtype=torch.float32 if k == "const_vecs" else w[k].dtype)
         if w.get("logit_bias") is not None:
             g["logit_bias"] = torch.empty(c.E, device=dev)
         if c.gate_residual_scale:
             g["z_prev"] = torch.empty(c.T, c.E, device=dev)
-        if cv is not None:
-            g["const_vecs"] = torch.empty(cv.shape, device=dev)
-        if c.n_shared:
-            g["Ws1"], g["Ws2"] = torch.empty_like(w["Ws1"]), torch.empty_like(w["Ws2"])
+        out = {k: g.get(k) if on else None for k, on in used.items()}
         combine_backward(c, dy, s["y_perm"], *routing, dy_perm, dw, self.status, self.bws,
-                         dconst=g.get("const_vecs"))
+                         dconst=out["const_vecs"])
         dx_perm = torch.empty_like(s["x_perm"])
         dx_shared = torch.empty_like(x) if c.n_shared else None
-        grouped_mlp_backward(c, s["x_perm"], s["offsets"], w["W1"], w["W2"], dy_perm, x, w.get("Ws1"),
-                             w.get("Ws2"), dy, self.status, self.bws, dx_perm=dx_perm, dW1=g["W1"],
-                             dW2=g["W2"], dx_shared=dx_shared, dWs1=g.get("Ws1"), dWs2=g.get("Ws2"))
+        grouped_mlp_backward(c, s["x_perm"], s["offsets"], W["W1"], W["W2"], dy_perm, x, W["Ws1"], W["Ws2"], dy,
+                             self.status, self.bws, dx_perm=dx_perm, dW1=out["W1"], dW2=out["W2"],
+                             dx_shared=dx_shared, dWs1=out["Ws1"], dWs2=out["Ws2"])
         dx_router = torch.empty_like(x)
         router_backward(c, x, w["W_r"], s["probs"], s["sel"], s["w"], dw, s["tok_ptr"], s["tok_assign"],
                         torch.empty_like(s["probs"]), self.status, self.bws, dprobs=dprobs,
