@@ -236,10 +236,10 @@ class CudaOps:
 
     def route(self, x, z_prev=None):
         T, E, k = x.shape[0], self.cfg["E"], self.cfg["k"]
-        logits = torch.empty(T, E, device=self.device)
-        probs = torch.empty(T, E, device=self.device)
+        logits = torch.empty(T, E, dtype=torch.float32, device=self.device)
+        probs = torch.empty(T, E, dtype=torch.float32, device=self.device)
         sel = torch.empty(T * k, dtype=torch.int32, device=self.device)
-        w = torch.empty(T * k, device=self.device)
+        w = torch.empty(T * k, dtype=torch.float32, device=self.device)
         self.m.router(x, self.W_r, logits, probs, bias=self.bias, z_prev=z_prev,
                       z_prev_scale=self.cfg.get("gate_residual_scale", 0.0), k=k,
                       renorm=self.cfg.get("renorm", 0), idx=sel, w=w)

@@ -628,9 +628,12 @@ class MoELayer:
         def ints(*shape):
             return torch.empty(*shape, dtype=i32, device=dev)
 
+        def floats(*shape):  # fp32 whatever torch's default type is: the kernels write 4 bytes
+            return torch.empty(*shape, dtype=torch.float32, device=dev)
+
         s = {"x": x, "residual": residual,
-             "logits": torch.empty(T, E, device=dev), "probs": torch.empty(T, E, device=dev),
-             "sel": ints(n), "w": torch.empty(n, device=dev), "offsets": ints(c.n_heavy + 1),
+             "logits": floats(T, E), "probs": floats(T, E),
+             "sel": ints(n), "w": floats(n), "offsets": ints(c.n_heavy + 1),
              "row_of": ints(n), "tok_ptr": ints(T + 1) if ec else None,
              "tok_assign": ints(n) if ec else None,
              "x_perm": torch.empty(n, c.d, dtype=x.dtype, device=dev),
@@ -671,22 +674,26 @@ class MoELayer:
     def _backward(self, saved, dy, dprobs, dlogits):
         c, w, s, dev = self.c, self.w, saved, dy.device
         n, x = num_assignments(c), saved["x"]
+
+        def floats(*shape):
+            return torch.empty(*shape, dtype=torch.float32, device=dev)
+
         # Weights that none of the layer's experts reads have gradient zero and go no further.
         used = {"W1": c.n_heavy > 0, "W2": c.n_heavy > 0, "Ws1": c.n_shared > 0, "Ws2": c.n_shared > 0,
                 "const_vecs": _n_const(c) > 0}
         W = {k: w.get(k) if on else None for k, on in used.items()}
         cv = W["const_vecs"]
         routing = (s["sel"], s["w"], s["row_of"], s["tok_ptr"], s["tok_assign"], x, cv)
-        dy_perm, dw = torch.empty_like(s["y_perm"]), torch.empty(n, device=dev)
-        g = {"W_r": torch.empty(c.E, c.d, device=dev), "x": torch.empty_like(x)}
+        dy_perm, dw = torch.empty_like(s["y_perm"]), floats(n)
+        g = {"W_r": floats(c.E, c.d), "x": torch.empty_like(x)}
         for k, on in used.items():
             if w.get(k) is not None:
                 new = torch.empty_like if on else torch.zeros_like
                 g[k] = new(w[k], dtype=torch.float32 if k == "const_vecs" else w[k].dtype)
         if w.get("logit_bias") is not None:
-            g["logit_bias"] = torch.empty(c.E, device=dev)
+            g["logit_bias"] = floats(c.E)
         if c.gate_residual_scale:
-            g["z_prev"] = torch.empty(c.T, c.E, device=dev)
+            g["z_prev"] = floats(c.T, c.E)
         out = {k: g.get(k) if on else None for k, on in used.items()}
         combine_backward(c, dy, s["y_perm"], *routing, dy_perm, dw, self.status, self.bws,
                          dconst=out["const_vecs"])
