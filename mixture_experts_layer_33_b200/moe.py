@@ -638,6 +638,9 @@ class MoELayer:
              "tok_assign": ints(n) if ec else None,
              "x_perm": torch.empty(n, c.d, dtype=x.dtype, device=dev),
              "y_perm": torch.empty(n, c.d, dtype=x.dtype, device=dev)}
+        if T == 0:  # no rows to route; the weights' gradients are zero
+            s["offsets"].zero_()
+            return torch.empty_like(x), s
         topk = c.routing == TOKEN_TOPK
         router(x, w["W_r"], s["logits"], s["probs"], bias=w.get("logit_bias"), z_prev=z_prev,
                z_prev_scale=c.gate_residual_scale, k=c.k if topk else 0, renorm=c.renorm if topk else 0,
