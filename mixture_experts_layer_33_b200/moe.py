@@ -622,6 +622,14 @@ class MoELayer:
 
     def _forward_train(self, x, z_prev, residual):
         c, w, dev, i32 = self.c, self.w, x.device, torch.int32
+        # The step's buffers have the config's sizes: a longer batch would be written past their ends.
+        dt, at = _layer_dtype(c), torch.cuda.current_device() if x.is_cuda else -1
+        if tuple(x.shape) != (c.T, c.d):
+            raise ValueError(f"x: expected [{c.T}, {c.d}], got {tuple(x.shape)}")
+        _grad_ptr(x, "x", dt, c.T * c.d, at)
+        _grad_ptr(z_prev, "z_prev", torch.float32, c.T * c.E, at)
+        if not isinstance(residual, str):
+            _grad_ptr(residual, "residual", dt, c.T * c.d, at)
         n, T, E = num_assignments(c), c.T, c.E
         ec = c.routing == EXPERT_CHOICE
 
