@@ -975,7 +975,10 @@ int row_threads(int d, int nv) {
 // time (the backward spills there: 12 arrays of 16 columns do not fit 128
 // registers).
 template <typename T> inline bool narrow(int d) { return d * (int)sizeof(T) <= 8192; }
-// The kernels for many rows are built for three bounds on the threads.
+// The kernels for many rows are built for three bounds on the threads (fp32
+// rows of up to 8 KB take at most 256). Their limit on shared memory is set to
+// the bound's: one that follows the size of each call could be lowered by
+// another host thread between a call's setting it and its launch.
 inline int thread_bound(int d) {
   const int t = row_threads(d, 1);
   return t <= 160 ? 160 : t <= 256 ? 256 : 512;
@@ -993,11 +996,12 @@ int run_fwd(const BlockNormArgs &a, cudaStream_t stream) {
     const NormPlan p = norm_plan(a.T, a.group, a.gate || a.scale || a.shift, kFwdRows,
                                  (int)sms * fwd_ctas(thread_bound(a.d)));
     const int threads = row_threads(a.d, 1), bound = thread_bound(a.d);
-    const auto kern = bound == 160   ? block_norm_vec_kernel<T, 160>
-                      : bound == 256 ? block_norm_vec_kernel<T, 256>
-                                     : block_norm_vec_kernel<T, 512>;
+    const auto kern = bound == 160                     ? block_norm_vec_kernel<T, 160>
+                      : bound == 256 || sizeof(T) == 4 ? block_norm_vec_kernel<T, 256>
+                                                       : block_norm_vec_kernel<T, sizeof(T) == 4 ? 256 : 512>;
     const size_t smem = fetch_bytes<T, 2 * kFwdRows, kFwdDepth>(threads);
-    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    const size_t most = fetch_bytes<T, 2 * kFwdRows, kFwdDepth>(bound);
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
     kern<<<p.grid, threads, smem, stream>>>(a, p);
   }
   return last_launch_status();
@@ -1012,9 +1016,9 @@ NormPlan bwd_plan(int tokens, int d, int group, bool conds) {
 
 template <typename T, bool POST>
 auto bwd_kernel(int bound) {
-  return bound == 160   ? block_norm_bwd_vec_kernel<T, POST, 160>
-         : bound == 256 ? block_norm_bwd_vec_kernel<T, POST, 256>
-                        : block_norm_bwd_vec_kernel<T, POST, 512>;
+  return bound == 160                     ? block_norm_bwd_vec_kernel<T, POST, 160>
+         : bound == 256 || sizeof(T) == 4 ? block_norm_bwd_vec_kernel<T, POST, 256>
+                                          : block_norm_bwd_vec_kernel<T, POST, sizeof(T) == 4 ? 256 : 512>;
 }
 
 template <typename T>
@@ -1032,7 +1036,8 @@ int run_bwd(const BlockNormArgs &a, cudaStream_t stream) {
       const int threads = row_threads(a.d, 1), bound = thread_bound(a.d);
       const auto kern = a.post == MOE_NORM_NONE ? bwd_kernel<T, false>(bound) : bwd_kernel<T, true>(bound);
       const size_t smem = fetch_bytes<T, 4 * kBwdRows, kBwdDepth>(threads);
-      MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      const size_t most = fetch_bytes<T, 4 * kBwdRows, kBwdDepth>(bound);
+      MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
       kern<<<p.grid, threads, smem, stream>>>(a, p, part, wpart);
     }
   }

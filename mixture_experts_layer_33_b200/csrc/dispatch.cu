@@ -318,7 +318,10 @@ int launch_dispatch(const DispatchArgs &a, void *ws, cudaStream_t stream) {
   if (st != MOE_OK) return st;
   if (a.routing == MOE_EXPERT_CHOICE && a.tok_ptr && a.tok_assign && a.T > 0) {
     const size_t smem = 2 * (size_t)a.S * sizeof(int);
-    MOE_CUDA_TRY(cudaFuncSetAttribute(token_csr_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    // The limit is the largest group's, not the call's: another host thread must
+    // not lower it between here and the launch.
+    MOE_CUDA_TRY(cudaFuncSetAttribute(token_csr_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      2 * kMaxGroup * (int)sizeof(int)));
     token_csr_kernel<<<a.T / a.S, kThreads, smem, stream>>>(a);
     st = last_launch_status();
   }

@@ -23,6 +23,7 @@ struct KindTable;
 // Experts per layer the library takes (moe_config.E; larger is
 // MOE_ERR_UNSUPPORTED).
 constexpr int kMaxLayerExperts = 128;
+constexpr int kMaxGroup = 16384;  // tokens of an expert-choice group
 
 inline int last_launch_status() {
   return cudaPeekAtLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

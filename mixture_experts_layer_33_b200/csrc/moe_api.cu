@@ -47,7 +47,7 @@ int check_config(const moe_config *c) {
     case MOE_EXPERT_CHOICE:
       if (c->group_size < 1 || c->T % c->group_size != 0) return MOE_ERR_INVALID_ARG;
       if (c->capacity < 1 || c->capacity > c->group_size) return MOE_ERR_INVALID_ARG;
-      if (c->group_size > 16384) return MOE_ERR_UNSUPPORTED;
+      if (c->group_size > kMaxGroup) return MOE_ERR_UNSUPPORTED;
       break;
     case MOE_DES_VOTE:
       if (c->k < 1 || c->k > c->M_core || c->M_core > c->E) return MOE_ERR_INVALID_ARG;
@@ -727,7 +727,7 @@ int moe_select_expert_choice(const float *probs, int T, int E, int group_size, i
                              int32_t *tok, float *w, moe_stream_t stream) {
   if (T < 0 || E < 1 || group_size < 1 || T % group_size != 0) return MOE_ERR_INVALID_ARG;
   if (C < 1 || C > group_size) return MOE_ERR_INVALID_ARG;
-  if (group_size > 16384) return MOE_ERR_UNSUPPORTED;
+  if (group_size > kMaxGroup) return MOE_ERR_UNSUPPORTED;
   if (!probs || !tok || !w) return MOE_ERR_INVALID_ARG;
   return launch_expert_choice(probs, T, E, group_size, C, tok, w, stream);
 }

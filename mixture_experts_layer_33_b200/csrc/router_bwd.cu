@@ -515,11 +515,12 @@ int launch_router_bwd(const RouterBwdArgs &a, cudaStream_t stream) {
       else if (a.E <= 64) st = run_bf16<4>(a, splits, bias_part, stream);
       else st = run_bf16<8>(a, splits, bias_part, stream);
     } else {
-      const size_t smem = (size_t)(TT * FC + TT * a.E + a.E * FC) * 4;
-      const auto kern = a.E <= 8    ? router_bwd_f32_kernel<2>
-                        : a.E <= 32 ? router_bwd_f32_kernel<8>
-                                    : router_bwd_f32_kernel<32>;
-      MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      const auto bytes = [](int E) { return (size_t)(TT * FC + TT * E + E * FC) * 4; };
+      const int ept = a.E <= 8 ? 2 : a.E <= 32 ? 8 : 32;
+      const auto kern = ept == 2 ? router_bwd_f32_kernel<2> : ept == 8 ? router_bwd_f32_kernel<8> : router_bwd_f32_kernel<32>;
+      const size_t smem = bytes(a.E);
+      // The limit is the variant's, not the call's: another host thread must not lower it before the launch.
+      MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(4 * ept)));
       launch_chained(kern, dim3((a.d + FC - 1) / FC, splits), kThreads, smem, stream, a, splits, bias_part);
       st = last_launch_status();
     }

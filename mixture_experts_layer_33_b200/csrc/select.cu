@@ -393,8 +393,10 @@ int launch_expert_choice(const float *probs, int T, int E, int S, int C, int32_t
   const int G = T / S;
   if (G == 0) return MOE_OK;
   const size_t smem = (size_t)S * sizeof(uint32_t);
-  MOE_CUDA_TRY(cudaFuncSetAttribute(expert_choice_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  // The limit is the largest group's, not the call's: another host thread must
+  // not lower it between here and the launch.
+  MOE_CUDA_TRY(cudaFuncSetAttribute(expert_choice_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMaxGroup * (int)sizeof(uint32_t)));
   int threads = S < kEcThreads ? ((S + 31) / 32) * 32 : kEcThreads;
   expert_choice_kernel<<<G * E, threads, smem, stream>>>(probs, E, S, C, tok, w);
   return last_launch_status();
