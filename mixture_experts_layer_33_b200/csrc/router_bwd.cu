@@ -243,18 +243,39 @@ __global__ void __launch_bounds__(kThreads) router_bwd_bf16_kernel(RouterBwdArgs
     if (want_w) {
       // dW_r[e][c] += sum_r dz[r][e] x[r][c]: A = dz^T (ldmatrix.trans on
       // [token][expert] rows), B = x (ldmatrix.trans on [token][column] rows).
+      // A tile's sums are formed on their own and then added in fp32: the
+      // tensor cores cut their sums off instead of rounding them, which over
+      // 65536 tokens of one sign left dW_r 4e-5 too small in one long chain.
+      constexpr int MG = MT < 2 ? MT : 2;  // experts in 16s at a time
+      uint32_t b[TT / 16][4];              // columns 16 warp + {0..7, 8..15}, k halves
 #pragma unroll
-      for (int k = 0; k < TT; k += 16) {
-        uint32_t b[4];  // columns 16 warp + {0..7, 8..15}, k halves
-        ldmatrix_x4_trans(b, sx + (k + (lane & 15)) * XP + warp * 16 + (lane >> 4) * 8);
+      for (int m0 = 0; m0 < MT; m0 += MG) {
+        float t[MG][2][4];
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
+        for (int m = 0; m < MG; ++m)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            uint32_t f[4];
-            ldmatrix_x4_trans(f, sz + (p * TT + k + (lane & 7) + ((lane >> 4) << 3)) * ZP + m * 16 + ((lane >> 3) & 1) * 8);
-            mma2(acc[m][0], acc[m][1], f, b);
-          }
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[m][n][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < TT; k += 16) {
+          if (m0 == 0) ldmatrix_x4_trans(b[k / 16], sx + (k + (lane & 15)) * XP + warp * 16 + (lane >> 4) * 8);
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int m = 0; m < MG; ++m) {
+              uint32_t f[4];
+              ldmatrix_x4_trans(f, sz + (p * TT + k + (lane & 7) + ((lane >> 4) << 3)) * ZP + (m0 + m) * 16 +
+                                       ((lane >> 3) & 1) * 8);
+              mma2(t[m][0], t[m][1], f, b[k / 16]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MG; ++m)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m0 + m][n][i] += t[m][n][i];
       }
     }
     if (want_x) {
