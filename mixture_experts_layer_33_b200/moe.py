@@ -615,8 +615,8 @@ class MoELayer:
 
     def forward_train(self, x, z_prev=None, residual="x", stream=None):
         """The layer through its stage entry points: (y, saved), ``saved`` holding the routing,
-        the dispatched rows and the expert outputs for ``backward``. ``residual`` is "x" (the
-        layer adds x), None, or another [T, d] tensor."""
+        the dispatched rows and the expert outputs for ``backward``. ``residual`` is "x" or x
+        itself (the layer adds x), None, or another [T, d] tensor. ``saved`` keeps x, not a copy."""
         return _run_on(stream, lambda: self._forward_train(x, z_prev, residual),
                        (x, z_prev, residual, self.ws, self.status))
 
@@ -639,7 +639,7 @@ class MoELayer:
         def floats(*shape):  # fp32 whatever torch's default type is: the kernels write 4 bytes
             return torch.empty(*shape, dtype=torch.float32, device=dev)
 
-        s = {"x": x, "residual": residual,
+        s = {"x": x, "residual": "x" if residual is x else residual,
              "logits": floats(T, E), "probs": floats(T, E),
              "sel": ints(n), "w": floats(n), "offsets": ints(c.n_heavy + 1),
              "row_of": ints(n), "tok_ptr": ints(T + 1) if ec else None,
