@@ -89,3 +89,32 @@ def test_results_dropped_while_the_caller_reads_them():
         assert torch.equal(ky, y0)
         for k in g0:
             assert torch.equal(kept[k], g0[k]), k
+
+
+@pytest.mark.parametrize("name", ["mmoe", "expert_choice"])
+def test_step_on_a_stream_forked_in_a_capture(name):
+    """Captured with stream= a stream forked from the capture's, replayed on new inputs in place."""
+    layer, x, z_prev, dy = setup(name)
+    x2 = torch.randn_like(x.float()).to(x.dtype)
+    x_in = x.clone()
+
+    def step(stream=None):
+        y, s = layer.forward_train(x_in, z_prev=z_prev, stream=stream)
+        return {"y": y, **layer.backward(s, dy, stream=stream)}
+    want = []
+    for v in (x, x2):
+        x_in.copy_(v)
+        want.append({k: t.clone() for k, t in step().items()})
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        held = step(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for k in range(4):
+        x_in.copy_((x, x2)[k % 2])
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in held.items():
+            assert torch.equal(t, want[k % 2][n]), (k, n)
+    assert int(layer.status.item()) == 0
