@@ -460,6 +460,8 @@ MOE_API int moe_forward_host(const moe_config *cfg, const void *x_host,
  * router, of constant experts, of norm weights and of conditions are fp32.
  * Every sum runs in a fixed order, so repeated calls give the same bits.
  * Outputs are written, not accumulated into.
+ * T, the assignments, the rows of W1 over all experts and the shared hidden
+ * width are at most 2^30 (MOE_ERR_UNSUPPORTED beyond).
  *
  * A training step of the layer (each step's inputs are the forward's):
  *   moe_combine_backward       dy -> dy_perm, dw, dconst

@@ -15,6 +15,17 @@ bool all_aligned16(P... p) {
   return (aligned16(p) && ...);
 }
 
+// The kernels count rows and tiles in 32 bits, a tile past the last row too.
+constexpr int64_t kMaxRows = 1 << 30;
+int check_bwd_config(const moe_config *cfg) {
+  const int st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  const int64_t w1_rows = (int64_t)cfg->n_heavy * cfg->h * (cfg->act == MOE_SWIGLU ? 2 : 1);
+  const int64_t shared = (int64_t)cfg->n_shared * cfg->h_shared;
+  if (cfg->T > kMaxRows || n_assign_of(*cfg) > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  return (cfg->n_heavy > 0 && w1_rows > kMaxRows) || shared > kMaxRows ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
 // Whether two buffers of `bytes` bytes share any.
 inline bool overlap(const void *a, const void *b, size_t bytes) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
@@ -93,7 +104,7 @@ using namespace moe;
 extern "C" {
 
 int moe_backward_workspace_size(const moe_config *cfg, size_t *bytes) {
-  const int st = check_config(cfg);
+  const int st = check_bwd_config(cfg);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_INVALID_ARG;
   *bytes = bwd_layout(*cfg).total;
@@ -103,7 +114,7 @@ int moe_backward_workspace_size(const moe_config *cfg, size_t *bytes) {
 int moe_combine_backward(const moe_config *cfg, const void *dy, const void *y_perm, const int32_t *sel, const float *w,
                          const int32_t *row_of, const void *x, const void *const_vecs, void *dy_perm, float *dw,
                          float *dconst, int32_t *dev_status, void *ws, size_t ws_bytes, moe_stream_t stream) {
-  int st = check_config(cfg);
+  int st = check_bwd_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config &c = *cfg;
   const int n_const = n_const_of(c);
@@ -125,7 +136,7 @@ int moe_dispatch_backward(const moe_config *cfg, const void *dx_perm, const void
                           const float *w, const int32_t *row_of, const int32_t *tok_ptr, const int32_t *tok_assign,
                           const void *x, const void *const_vecs, const void *add0, const void *add1, const void *add2,
                           void *dx, int32_t *dev_status, moe_stream_t stream) {
-  const int st = check_config(cfg);
+  const int st = check_bwd_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config &c = *cfg;
   const bool mix = n_const_of(c) > 0 && c.const_mix;
@@ -158,7 +169,7 @@ int moe_router_backward_logits(const moe_config *cfg, const void *x, const void 
                                 const int32_t *tok_assign, const float *dprobs, const float *dz_next, float *dlogits,
                                 float *dz_prev, float *dbias, float *dW_r, void *dx, int32_t *dev_status, void *ws,
                                 size_t ws_bytes, moe_stream_t stream) {
-  int st = check_config(cfg);
+  int st = check_bwd_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config &c = *cfg;
   if (c.T > 0) {
@@ -185,12 +196,11 @@ int moe_grouped_mlp_backward(const moe_config *cfg, const void *x_perm, const in
                              const void *W2, const void *dy_perm, const void *x, const void *Ws1, const void *Ws2,
                              const void *dy_shared, void *dx_perm, void *dW1, void *dW2, void *dx_shared, void *dWs1,
                              void *dWs2, int32_t *dev_status, void *ws, size_t ws_bytes, moe_stream_t stream) {
-  int st = check_config(cfg);
+  int st = check_bwd_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config &c = *cfg;
   const int64_t na = n_assign_of(c), hs = (int64_t)c.n_shared * c.h_shared;
   const bool routed = c.n_heavy > 0 && (dx_perm || dW1 || dW2), shared = hs > 0 && (dx_shared || dWs1 || dWs2);
-  if (hs > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   if (routed && (!offsets || !W1 || !W2 || (na > 0 && (!x_perm || !dy_perm)))) return MOE_ERR_INVALID_ARG;
   if (shared && (!Ws1 || !Ws2 || (c.T > 0 && (!x || !dy_shared)))) return MOE_ERR_INVALID_ARG;
   if (!all_aligned16(x_perm, W1, W2, dy_perm, x, Ws1, Ws2, dy_shared) ||
