@@ -23,6 +23,8 @@
 // and more columns: too few warps fit an SM to hide their latencies
 // (8192 x 1152, LayerNorm: forward 24 us, backward 50-55 us, against 16 and
 // 25 + 4.5 here; elementwise kernels over as many bytes take 12.9 and 18.4).
+// That is bf16; fp32 rows of the same width have rings twice as large, which
+// leave 2 CTAs an SM forward and 1 backward instead of the planned 4 and 3.
 // Variances are sums of squares of centred values (two reductions), not
 // differences of moments: with a mean of 100 standard deviations the latter
 // would lose 4 digits. Everything between the loads and the stores is fp32,
@@ -972,8 +974,8 @@ int row_threads(int d, int nv) {
 }
 // Rows of up to 8 KB take a thread per 8 columns (at most 512 threads, and
 // rings of at most 196 KB); wider ones 2 vectors per thread and one row at a
-// time (the backward spills there: 12 arrays of 16 columns do not fit 128
-// registers).
+// time (the backward spills 512 bytes a thread there: 12 arrays of 16 columns
+// do not fit 128 registers).
 template <typename T> inline bool narrow(int d) { return d * (int)sizeof(T) <= 8192; }
 // The kernels for many rows are built for three bounds on the threads (fp32
 // rows of up to 8 KB take at most 256). Their limit on shared memory is set to
@@ -1007,7 +1009,9 @@ int run_fwd(const BlockNormArgs &a, cudaStream_t stream) {
   return last_launch_status();
 }
 
-// Rows at a time and CTAs at once of the backward.
+// Rows at a time and CTAs at once of the backward. The SMs are counted as the
+// B200's 148, not asked for: the plan sizes the workspace, which has to be the
+// same on a host without a GPU, and fixes the order of the sums.
 template <typename T>
 NormPlan bwd_plan(int tokens, int d, int group, bool conds) {
   return narrow<T>(d) ? norm_plan(tokens, group, conds, kBwdRows, 148 * bwd_ctas(thread_bound(d)))

@@ -321,10 +321,12 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices / 4) const_grad_sum_kern
 // that out) its Wc rows with coefficient q, and the coefficient of dy_s. The
 // chain token list -> assignment -> row -> values is four round trips; warps
 // enough to hide it stay resident only with few registers, so two chunks and
-// BATCH slots at a time. 8192 tokens of 2048 under expert choice with two
-// added gradients (168 MB): 38 us, where a copy of as many bytes takes 35. A
-// warp that walks the lists ahead of the others took 45 us, four chunks a warp
-// or four tokens in a row 43, one chunk and more warps 42.
+// BATCH slots at a time (at 62 registers it spills 64 bytes a thread; the mixed
+// forms, at 128, up to 96). 8192 tokens of 2048 under expert choice with two
+// added gradients (168 MB): 37.8 us in a graph, 0.69 of what an elementwise
+// kernel over as many bytes makes of it (26.3). A warp that walks the lists
+// ahead of the others took 45 us, four chunks a warp or four tokens in a row
+// 43, one chunk and more warps 42.
 template <bool MIX> struct Slot {
   int row;    // of dx_perm; -1: no source; -2 - c: mixed constant expert c
   float own;  // coefficient of dy_s: w of an identity, w a0 of a mixed constant expert

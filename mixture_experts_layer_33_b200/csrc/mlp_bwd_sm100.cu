@@ -16,7 +16,9 @@
 //              is written to memory or rounded: while the dH product runs,
 //              the epilogue turns U into H (stored) and act'(U), which it
 //              holds in fp32 registers; when dH is done it stores the
-//              product. The next tile's U overlaps that second half.
+//              product. The next tile's U overlaps that second half. (At
+//              the 168 registers that ten warps can have it spills 120
+//              bytes a thread, 180 for SwiGLU.)
 //   dX         rows ragged, K = hidden width, two accumulators in turn.
 //   dW         both weight gradients (K = the group's rows) in one launch;
 //              small groups' dX and dW side by side in one.

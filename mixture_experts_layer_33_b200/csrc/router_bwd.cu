@@ -18,11 +18,11 @@
 // bf16 layers multiply on bf16 mma.sync (as the router's forward does: N = E
 // is far too narrow for a tcgen05 tile). dz is fp32 and enters as the sum of
 // three bf16 terms (8 mantissa bits each, 24 in all), so the products keep
-// fp32 accuracy while x and W_r are exact. 8192 x 1152, 19 experts: 24.7 us, 22.1
+// fp32 accuracy while x and W_r are exact. 8192 x 1152, 19 experts: 24.6 us, 22.6
 // in a graph, where an elementwise kernel over as many bytes takes 7.7; launched
-// apart 6.4 + 17.8 + 4, the middle one with the tensor pipe 44 % and L1 65 % busy
-// (three terms, experts padded to 32). The terms one after the other along K
-// (4 steps of 16 instead of 6) took 24.6 us in a graph against 23.5 then.
+// apart and cold 7.4 + 19.7 + 6.0, the middle one with the tensor pipe 43 % and L1
+// 64 % busy (three terms, experts padded to 32). The terms one after the other
+// along K (4 steps of 16 instead of 6) took 24.6 us in a graph against 23.5 then.
 #include "backward.h"
 #include "chained.cuh"
 #include "mma_sync.cuh"
@@ -491,7 +491,9 @@ __global__ void __launch_bounds__(kSumThreads) router_bwd_sum_kernel(const float
 }
 
 // Token ranges: as many CTAs with the columns as run at once (two per SM), at least one tile
-// each, and no more partial dW_r blocks than half the bytes of x.
+// each, and no more partial dW_r blocks than half the bytes of x. The SMs are counted as the
+// B200's 148, not asked for: the ranges size the workspace, which has to be the same on a
+// host without a GPU, and fix the order of the sums.
 int token_splits(int T, int d, int E, int dtype) {
   const int cols = dtype == MOE_BF16 ? TC : FC, eb = dtype == MOE_BF16 ? 2 : 4;
   const int64_t tiles = (T + TT - 1) / TT, blocks = (d + cols - 1) / cols;
