@@ -467,11 +467,12 @@ MOE_API int moe_forward_host(const moe_config *cfg, const void *x_host,
  *   moe_combine_backward       dy -> dy_perm, dw, dconst
  *   moe_grouped_mlp_backward   dy_perm, dy -> dx_perm, dW1, dW2, dx_shared, ...
  *   moe_router_backward        dw -> dlogits, dz_prev, dbias, dW_r, dx_router
+ *     (moe_router_backward_logits where the next layer's dz_prev comes back)
  *   moe_dispatch_backward      dx_perm + dx_shared + dx_router + dy -> dx
  */
 
-/* Workspace bytes the four backward entry points need for `cfg` (one buffer
- * of this size serves them one after the other). */
+/* Workspace bytes the backward entry points need for `cfg` (one buffer of
+ * this size serves them one after the other). */
 MOE_API int moe_backward_workspace_size(const moe_config *cfg, size_t *bytes);
 
 /*
@@ -671,6 +672,5 @@ MOE_API int moe_block_norm_backward(const moe_norm_config *cfg, const void *h, c
 #ifdef __cplusplus
 }
 #endif
-
 
 #endif /* MOE_H_ */

@@ -32,7 +32,7 @@ inline bool overlap(const void *a, const void *b, size_t bytes) {
   return (p < q ? q - p : p - q) < bytes;
 }
 
-// One workspace for the four backward entry points, which run one after
+// One workspace for the backward entry points, which run one after
 // another: each takes it from the start.
 struct BwdLayout {
   size_t H, dU, Hs, dUs, U, total;  // grouped MLP (routed, shared); the others use it whole
@@ -161,14 +161,14 @@ int moe_router_backward(const moe_config *cfg, const void *x, const void *W_r, c
                         const float *dprobs, float *dlogits, float *dz_prev, float *dbias, float *dW_r, void *dx,
                         int32_t *dev_status, void *ws, size_t ws_bytes, moe_stream_t stream) {
   return moe_router_backward_logits(cfg, x, W_r, probs, sel, w, dw, tok_ptr, tok_assign, dprobs, nullptr, dlogits,
-                                     dz_prev, dbias, dW_r, dx, dev_status, ws, ws_bytes, stream);
+                                    dz_prev, dbias, dW_r, dx, dev_status, ws, ws_bytes, stream);
 }
 
 int moe_router_backward_logits(const moe_config *cfg, const void *x, const void *W_r, const float *probs,
-                                const int32_t *sel, const float *w, const float *dw, const int32_t *tok_ptr,
-                                const int32_t *tok_assign, const float *dprobs, const float *dz_next, float *dlogits,
-                                float *dz_prev, float *dbias, float *dW_r, void *dx, int32_t *dev_status, void *ws,
-                                size_t ws_bytes, moe_stream_t stream) {
+                               const int32_t *sel, const float *w, const float *dw, const int32_t *tok_ptr,
+                               const int32_t *tok_assign, const float *dprobs, const float *dz_next, float *dlogits,
+                               float *dz_prev, float *dbias, float *dW_r, void *dx, int32_t *dev_status, void *ws,
+                               size_t ws_bytes, moe_stream_t stream) {
   int st = check_bwd_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config &c = *cfg;

@@ -385,7 +385,7 @@ def backward_workspace_size(c: MoeConfig) -> int:
 
 
 def alloc_backward_workspace(c: MoeConfig, device="cuda"):
-    """A caller-owned workspace for the four backward entry points, which may share it as long
+    """A caller-owned workspace for the backward entry points, which may share it as long
     as they do not overlap on the device."""
     return torch.empty(backward_workspace_size(c), dtype=torch.uint8, device=device)
 
