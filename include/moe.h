@@ -587,6 +587,8 @@ MOE_API int moe_router_backward_logits(const moe_config *cfg, const void *x, con
  *   dx_shared [T, d] out
  * Any output may be NULL: its product is left out. When all routed (or all
  * shared) outputs are NULL their inputs may be too.
+ * fp32 layers: at most 65535 tiles of 64 rows (one more per expert counted),
+ * of d and of W1's rows (MOE_ERR_UNSUPPORTED beyond, as from 4.19 million rows).
  * No output may overlap an input or another output: the products that read
  * the inputs and those that write the outputs may run at the same time.
  */

@@ -72,8 +72,8 @@ struct MlpBwdProblem {
   void *U;                 // workspace of the fp32 path: [rows, gated ? 2h : h] fp32
   int32_t *status;
 };
-// mlp_bwd_f32.cu: fp32 layers, on CUDA cores.
-int launch_mlp_bwd_f32(const MlpBwdProblem &p, cudaStream_t stream);
+// mlp_bwd_f32.cu: fp32 layers, on CUDA cores, one problem after the other.
+int launch_mlp_bwd_f32(const MlpBwdProblem *p, int n, cudaStream_t stream);
 // mlp_bwd_sm100.cu: bf16 layers on tcgen05, up to two problems in each launch.
 int launch_mlp_bwd_bf16(const MlpBwdProblem *q, int n, int32_t *status, cudaStream_t stream);
 

@@ -230,9 +230,7 @@ int moe_grouped_mlp_backward(const moe_config *cfg, const void *x_perm, const in
     p[i].dU = at<void>(ws, first ? L.dU : L.dUs);
     p[i].U = at<void>(ws, L.U);
   }
-  if (c.dtype == MOE_BF16) return launch_mlp_bwd_bf16(p, n, dev_status, stream);
-  for (int i = 0; i < n && st == MOE_OK; ++i) st = launch_mlp_bwd_f32(p[i], stream);
-  return st;
+  return c.dtype == MOE_BF16 ? launch_mlp_bwd_bf16(p, n, dev_status, stream) : launch_mlp_bwd_f32(p, n, stream);
 }
 
 int moe_block_norm(const moe_norm_config *cfg, const void *h, const void *x, const void *post_gamma, const void *gate,

@@ -138,11 +138,14 @@ __global__ void __launch_bounds__(kThreads) mlp_bwd_gemm_kernel(Gemm p) {
   }
 }
 
+inline unsigned tiles(int n) { return (unsigned)(((int64_t)n + kBN - 1) / kBN); }
+inline int64_t row_tiles(const MlpBwdProblem &p) {
+  return (p.rows + kBM - 1) / kBM + (p.offsets ? p.n_groups : 0);
+}
+
 int run(const MlpBwdProblem &p, cudaStream_t stream) {
   const int up = p.gated ? 2 * p.h : p.h;
-  const int64_t mt = (p.rows + kBM - 1) / kBM + (p.offsets ? p.n_groups : 0);
-  auto tiles = [](int n) { return (unsigned)((n + kBN - 1) / kBN); };
-  if (mt > 65535 || tiles(up) > 65535 || tiles(p.d) > 65535) return MOE_ERR_UNSUPPORTED;  // grid.y
+  const int64_t mt = row_tiles(p);
   Gemm g{};
   g.offsets = p.offsets; g.n_groups = p.n_groups; g.rows = p.rows; g.gated = p.gated; g.status = p.status;
   g.U = static_cast<float *>(p.U); g.H = p.H; g.dU = p.dU;
@@ -181,6 +184,13 @@ int run(const MlpBwdProblem &p, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_mlp_bwd_f32(const MlpBwdProblem &p, cudaStream_t stream) { return run(p, stream); }
+int launch_mlp_bwd_f32(const MlpBwdProblem *p, int n, cudaStream_t stream) {
+  for (int i = 0; i < n; ++i)  // grid.y; before either launches
+    if (row_tiles(p[i]) > 65535 || tiles(p[i].gated ? 2 * p[i].h : p[i].h) > 65535 || tiles(p[i].d) > 65535)
+      return MOE_ERR_UNSUPPORTED;
+  int st = MOE_OK;
+  for (int i = 0; i < n && st == MOE_OK; ++i) st = run(p[i], stream);
+  return st;
+}
 
 }  // namespace moe

@@ -46,3 +46,23 @@ def test_beyond_the_limit(m, kw):
 @pytest.mark.parametrize("kw", AT, ids=str)
 def test_at_the_limit(m, kw):
     assert m.backward_workspace_size(config(m, **kw)) > 0
+
+
+WS = 1 << 50  # more than any workspace: the pointers are not used either
+LARGE_F32 = {
+    "rows": dict(T=65532 * 64, k=1),
+    "rows_of_k": dict(T=65532 * 32, k=2),
+    # Few routed rows and too many of the shared expert: refused before the routed part is launched.
+    "shared_rows": dict(T=65536 * 64, routing="expert_choice", group_size=16384, capacity=1, n_shared=1, h_shared=8),
+    "shared_width": dict(T=65536, routing="expert_choice", group_size=16384, capacity=1, n_shared=1,
+                         h_shared=65536 * 64),
+    "width": dict(h=65536 * 64),
+}
+
+
+@pytest.mark.parametrize("name", list(LARGE_F32))
+def test_fp32_mlp_tiles(m, name):
+    c = config(m, dtype="f32", **LARGE_F32[name])
+    assert m.backward_workspace_size(c) < WS
+    code = m.LIB.moe_grouped_mlp_backward(ctypes.byref(c), *[FAKE] * 16, FAKE, WS, None)
+    assert code == UNSUPPORTED
